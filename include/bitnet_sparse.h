@@ -346,6 +346,27 @@ bitnet_status bitnet_rmsnorm_quant(const void *X, const float *w, int64_t T, int
                                    float eps_act, int8_t *Xq, float *absmax, float *rinv, bitnet_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * bitnet_add_rmsnorm_quant - residual addition, RMSNorm and the per-token
+ * quantisation in one pass.
+ *
+ * The pre-norm block adds a product's output to the residual stream and
+ * normalises the sum for the next product ("BitNet b1.58 ...", section "What
+ * this paper explains": LLaMA-alike blocks):
+ *   H[t,k] = bf16(fp32(X[t,k] + R[t,k]))   (the nearest bf16 of the exact sum);
+ *   Xq, absmax, rinv = bitnet_rmsnorm_quant(H, w, ...), bit for bit.
+ *
+ *   X, R     [T, K] bf16, 16-byte aligned: the product's output and the
+ *            residual stream.  K % 8 == 0, K <= 65536.
+ *   H        [T, K] bf16 out, 16-byte aligned: the new residual stream.  It may
+ *            be X or R itself (in place); any other overlap is refused.
+ *   w, eps_norm, eps_act, Xq, absmax, rinv   as bitnet_rmsnorm_quant.
+ * Errors: INVALID_ARG, UNSUPPORTED (T >= 2^31), CUDA.
+ * ------------------------------------------------------------------------ */
+bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float *w, int64_t T, int64_t K,
+                                       float eps_norm, float eps_act, void *H, int8_t *Xq, float *absmax, float *rinv,
+                                       bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * bitnet_swiglu_quant - SwiGLU gate fused into the per-token quantisation.
  *
  * Same pages and sections as bitnet_rmsnorm_quant.  Per token t and column f:

@@ -29,7 +29,7 @@ EXPORTED = [
     "bitnet_pack_update_workspace_size", "bitnet_pack_nm_update",
     "bitnet_pack_update_batch_workspace_size", "bitnet_pack_nm_update_batch",
     "bitnet_pack_6of8_windows", "bitnet_quant_act_lift_6of8",
-    "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_swiglu_quant",
+    "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_add_rmsnorm_quant", "bitnet_swiglu_quant",
     "bitnet_linear_workspace_size", "bitnet_sparse_linear",
     "bitnet_quant_linear_workspace_size", "bitnet_quant_linear",
     "bitnet_decode_chain_workspace_size", "bitnet_decode_chain",
@@ -119,6 +119,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "bitnet_quant_act_lift_6of8": (I32, [P, I32, I64, I64, F, P, P, P]),
         "bitnet_quant_act": (I32, [P, I32, I64, I64, F, P, P, P]),
         "bitnet_rmsnorm_quant": (I32, [P, P, I64, I64, F, F, P, P, P, P]),
+        "bitnet_add_rmsnorm_quant": (I32, [P, P, P, I64, I64, F, F, P, P, P, P, P]),
         "bitnet_swiglu_quant": (I32, [P, P, I64, I64, I64, F, P, P, P]),
         "bitnet_linear_workspace_size": (SZ, []),
         "bitnet_sparse_linear": (I32, [P, P, ctypes.POINTER(BitnetPackedW), I64, P, I32, P, P, SZ, P]),
@@ -171,6 +172,39 @@ def _stream(stream=None):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _launch(name: str, like, stream, *args) -> None:
+    """Calls the entry point `name` with args and the stream, on the device of the
+    tensor `like`: the current stream of that device unless one is given."""
+    torch = _torch()
+    index = like.device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(name, like, stream, *args)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    check(getattr(load(), name)(*args, s.cuda_stream), name)
+
+
+def _new(shape, dtype, like, stream):
+    """An uninitialised tensor on like's device that belongs to the stream the
+    kernels run on, so that the allocator reuses it in that stream's order."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _is(t, dtype, shape, like, optional=False) -> bool:
+    """t is a contiguous tensor of that type and shape on like's device (or None, where optional)."""
+    if t is None:
+        return optional
+    return t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == like.device
 
 
 def _dtype_code(dt) -> int:
@@ -425,6 +459,25 @@ def bitnet_rmsnorm_quant(X, w=None, eps_norm: float = 1e-6, eps_act: float = 1e-
     check(lib.bitnet_rmsnorm_quant(_ptr(X), _ptr(w), T, K, ctypes.c_float(eps_norm), ctypes.c_float(eps_act),
                                    _ptr(Xq), _ptr(absmax), _ptr(rinv), _stream(stream)), "bitnet_rmsnorm_quant")
     return Xq, absmax
+
+
+def bitnet_add_rmsnorm_quant(X, R, w=None, eps_norm: float = 1e-6, eps_act: float = 1e-5, H=None, Xq=None, absmax=None,
+                             rinv=None, stream=None):
+    """H = bf16(X + R) (bf16 [T, K]; H may be X or R), then bitnet_rmsnorm_quant of H.
+    Returns (H, Xq, absmax, rinv)."""
+    torch = _torch()
+    T, K = X.shape
+    assert _is(X, torch.bfloat16, (T, K), X) and X.is_cuda and _is(R, torch.bfloat16, (T, K), X)
+    assert _is(w, torch.float32, (K,), X, optional=True)
+    H = _new((T, K), torch.bfloat16, X, stream) if H is None else H
+    Xq = _new((T, K), torch.int8, X, stream) if Xq is None else Xq
+    absmax = _new((T,), torch.float32, X, stream) if absmax is None else absmax
+    rinv = _new((T,), torch.float32, X, stream) if rinv is None else rinv
+    assert _is(H, torch.bfloat16, (T, K), X) and _is(Xq, torch.int8, (T, K), X)
+    assert _is(absmax, torch.float32, (T,), X) and _is(rinv, torch.float32, (T,), X)
+    _launch("bitnet_add_rmsnorm_quant", X, stream, X.data_ptr(), R.data_ptr(), _addr(w), T, K, eps_norm, eps_act,
+            H.data_ptr(), Xq.data_ptr(), absmax.data_ptr(), rinv.data_ptr())
+    return H, Xq, absmax, rinv
 
 
 def bitnet_swiglu_quant(GU, F: int | None = None, eps_act: float = 1e-5, Xq=None, absmax=None, stream=None):

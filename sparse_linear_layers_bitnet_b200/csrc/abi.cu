@@ -29,6 +29,12 @@ bitnet_status cuda_status(cudaError_t e, const char *what) {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// whether [a, a + na) and [b, b + nb) share a byte
+bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
@@ -329,6 +335,26 @@ bitnet_status bitnet_rmsnorm_quant(const void *X, const float *w, int64_t T, int
     return cuda_status(bitnet::launch_rmsnorm_quant(X, w, T, K, eps_norm, eps_act, Xq, absmax, rinv,
                                                     reinterpret_cast<cudaStream_t>(stream)),
                        "rmsnorm_quant");
+}
+
+bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float *w, int64_t T, int64_t K,
+                                       float eps_norm, float eps_act, void *H, int8_t *Xq, float *absmax, float *rinv,
+                                       bitnet_stream_t stream) {
+    if (T < 0 || K <= 0 || K % 8 || K > 65536) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: need T >= 0, 0 < K <= 65536, K %% 8 == 0");
+    if (!(eps_norm > 0.0f) || !(eps_act > 0.0f)) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: eps must be > 0");
+    if (T == 0) return BITNET_OK;
+    if (!X || !R || !H || !Xq || !absmax) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: null pointer");
+    if (!aligned(X, 16) || !aligned(R, 16) || !aligned(H, 16) || !aligned(Xq, 16))
+        return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: X, R, H and Xq must be 16-byte aligned");
+    if (w && !aligned(w, 4)) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: w must be 4-byte aligned");
+    if (T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "add_rmsnorm_quant: T too large");
+    const size_t bytes = static_cast<size_t>(T) * static_cast<size_t>(K) * 2;
+    if ((H != X && overlaps(H, bytes, X, bytes)) || (H != R && overlaps(H, bytes, R, bytes)) ||
+        overlaps(Xq, bytes / 2, X, bytes) || overlaps(Xq, bytes / 2, R, bytes) || overlaps(Xq, bytes / 2, H, bytes))
+        return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: H may be X or R, no other overlap is allowed");
+    return cuda_status(bitnet::launch_add_rmsnorm_quant(X, R, w, T, K, eps_norm, eps_act, H, Xq, absmax, rinv,
+                                                        reinterpret_cast<cudaStream_t>(stream)),
+                       "add_rmsnorm_quant");
 }
 
 bitnet_status bitnet_swiglu_quant(const void *G, const void *U, int64_t ld, int64_t T, int64_t F, float eps_act,

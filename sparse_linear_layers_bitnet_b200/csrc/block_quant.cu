@@ -131,9 +131,9 @@ __device__ __forceinline__ float exp32(float x) {
     return __fmul_rn(p, __int_as_float((ni + 127) << 23));
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t *p, int64_t i) {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16);
-}
+__device__ __forceinline__ float bf16_of(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+__device__ __forceinline__ float bf16_at(const uint16_t *p, int64_t i) { return bf16_of(__ldg(p + i)); }
 
 __device__ __forceinline__ float bq_block_max(float v, float *s_red) {
 #pragma unroll
@@ -163,11 +163,26 @@ __device__ __forceinline__ uint32_t bq_code(float v, float s) {
     return static_cast<uint32_t>(q) & 0xffu;
 }
 
+// bf16(x + r) of two packed pairs: each sum is rounded to fp32, then to bf16.
+// (Two bf16 values whose exponents are at most 16 apart add exactly in fp32;
+// further apart the sum rounds back to the larger one either way, so this is
+// the nearest bf16 of the exact sum.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t x, uint32_t r) {
+    const float lo = __fadd_rn(__uint_as_float(x << 16), __uint_as_float(r << 16));
+    const float hi = __fadd_rn(__uint_as_float(x & 0xffff0000u), __uint_as_float(r & 0xffff0000u));
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // RMSNorm -> int8, one CTA per token.  X bf16 [T, K], optional fp32 weight w [K].
 // Pass 1 sums x^2 exactly; thread 0 forms r; pass 2 normalises, takes the
 // absmax; pass 3 writes the codes (the row is re-read from L1/L2).  rinv, when
 // given, receives r per token (what the backward of the norm needs).
-__global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *__restrict__ X, const float *__restrict__ w,
+// ADD: the normed row is bf16(X + R); pass 1 writes it to H (which may be X or
+// R: a thread writes only what it alone has read) and passes 2 and 3 read H.
+template <bool ADD>
+__global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *X, const uint16_t *R, uint16_t *H,
+                                                              const float *__restrict__ w,
                                                               int64_t K, float eps_n, float eps_a,
                                                               int8_t *__restrict__ Xq, float *__restrict__ amax,
                                                               float *__restrict__ rinv) {
@@ -188,7 +203,12 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *__
     uint64_t lo = 0, hi = 0;
     const int64_t nchunk = K / 8;   // 8 bf16 = 16 bytes
     for (int64_t c = threadIdx.x; c < nchunk; c += kBqThreads) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row) + c);
+        uint4 u = ADD ? reinterpret_cast<const uint4 *>(row)[c] : __ldg(reinterpret_cast<const uint4 *>(row) + c);
+        if (ADD) {
+            const uint4 v = reinterpret_cast<const uint4 *>(R + t * K)[c];
+            u = make_uint4(add_bf16x2(u.x, v.x), add_bf16x2(u.y, v.y), add_bf16x2(u.z, v.z), add_bf16x2(u.w, v.w));
+            reinterpret_cast<uint4 *>(H + t * K)[c] = u;
+        }
         const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -214,11 +234,12 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *__
         s_r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
         if (rinv) rinv[t] = s_r;
     }
-    __syncthreads();
+    __syncthreads();   // also orders the writes of H before the reads below
+    if (ADD) row = H + t * K;
     const float r = s_r;
     float m = 0.0f;
     for (int64_t i = threadIdx.x; i < K; i += kBqThreads) {
-        float v = __fmul_rn(bf16_at(row, i), r);
+        float v = __fmul_rn((ADD ? bf16_of(row[i]) : bf16_at(row, i)), r);
         if (w) v = __fmul_rn(v, __ldg(w + i));
         m = fmaxf(m, fabsf(v));
     }
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *__
         uint32_t q = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float v = __fmul_rn(bf16_at(row, i0 + j), r);
+            float v = __fmul_rn((ADD ? bf16_of(row[i0 + j]) : bf16_at(row, i0 + j)), r);
             if (w) v = __fmul_rn(v, __ldg(w + i0 + j));
             q |= bq_code(v, s) << (8 * j);
         }
@@ -390,8 +411,12 @@ __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
     return r;   // every warp reduces the same values: no second barrier needed
 }
 
-template <int CPT>
-__global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *__restrict__ X, const float4 *__restrict__ w,
+// ADD: the row is bf16(X + R), formed in registers from both rows' loads and
+// written to H once (H may be X or R: a thread writes only what it alone has
+// read).  Per element 2 + 2 bytes in and 2 + 1 out.
+template <int CPT, bool ADD>
+__global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *X, const uint4 *R, uint4 *H,
+                                                         const float4 *__restrict__ w,
                                                          int K, float eps_n, float eps_a,
                                                          int8_t *__restrict__ Xq, float *__restrict__ amax,
                                                          float *__restrict__ rinv) {
@@ -409,7 +434,22 @@ __global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *__restric
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
         const int c = threadIdx.x + j * blockDim.x;
-        v[j] = c < nchunk ? __ldg(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        v[j] = c < nchunk ? (ADD ? row[c] : __ldg(row + c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (ADD) {
+        uint4 u[CPT];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            u[j] = c < nchunk ? R[t * nchunk + c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            v[j] = make_uint4(add_bf16x2(v[j].x, u[j].x), add_bf16x2(v[j].y, u[j].y), add_bf16x2(v[j].z, u[j].z),
+                              add_bf16x2(v[j].w, u[j].w));
+            if (c < nchunk) H[t * nchunk + c] = v[j];
+        }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint64_t lo = 0, hi = 0;
@@ -623,15 +663,17 @@ static int pick_cpt(int64_t nchunk, const int *list, int n, int max_threads, int
 constexpr int kRmsCpt[] = {1, 2, 3, 4, 6, 8};   // larger CPT spills registers
 constexpr int kSwiCpt[] = {1, 2, 3, 4, 6, 8};
 
-template <int CPT>
-static cudaError_t rms_rc(cudaLaunchConfig_t &cfg, const void *X, const float *w, int64_t K, float eps_n, float eps_a,
-                          int8_t *Xq, float *amax, float *rinv) {
-    return cudaLaunchKernelEx(&cfg, k_rmsnorm_quant_rc<CPT>, static_cast<const uint4 *>(X),
+template <int CPT, bool ADD>
+static cudaError_t rms_rc(cudaLaunchConfig_t &cfg, const void *X, const void *R, void *H, const float *w, int64_t K,
+                          float eps_n, float eps_a, int8_t *Xq, float *amax, float *rinv) {
+    return cudaLaunchKernelEx(&cfg, k_rmsnorm_quant_rc<CPT, ADD>, static_cast<const uint4 *>(X),
+                              static_cast<const uint4 *>(R), static_cast<uint4 *>(H),
                               reinterpret_cast<const float4 *>(w), static_cast<int>(K), eps_n, eps_a, Xq, amax, rinv);
 }
 
-cudaError_t launch_rmsnorm_quant(const void *X, const float *w, int64_t T, int64_t K, float eps_n, float eps_a,
-                                 int8_t *Xq, float *amax, float *rinv, cudaStream_t s) {
+template <bool ADD>
+static cudaError_t rms_launch(const void *X, const void *R, void *H, const float *w, int64_t T, int64_t K, float eps_n,
+                              float eps_a, int8_t *Xq, float *amax, float *rinv, cudaStream_t s) {
     if (T <= 0) return cudaSuccess;
     cudaLaunchAttribute attr[1];
     int threads = 0;
@@ -642,18 +684,29 @@ cudaError_t launch_rmsnorm_quant(const void *X, const float *w, int64_t T, int64
     }
     if (cpt == 0) {   // rows beyond the register cache, or a weight vector without 16-byte alignment
         cudaLaunchConfig_t cfg = bq_config(T, kBqThreads, 0, s, attr);
-        return cudaLaunchKernelEx(&cfg, k_rmsnorm_quant, static_cast<const uint16_t *>(X), w, K, eps_n, eps_a, Xq,
+        return cudaLaunchKernelEx(&cfg, k_rmsnorm_quant<ADD>, static_cast<const uint16_t *>(X),
+                                  static_cast<const uint16_t *>(R), static_cast<uint16_t *>(H), w, K, eps_n, eps_a, Xq,
                                   amax, rinv);
     }
     cudaLaunchConfig_t cfg = bq_config(T, threads, 0, s, attr);
     switch (cpt) {
-        case 1: return rms_rc<1>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
-        case 2: return rms_rc<2>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
-        case 3: return rms_rc<3>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
-        case 4: return rms_rc<4>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
-        case 6: return rms_rc<6>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
-        default: return rms_rc<8>(cfg, X, w, K, eps_n, eps_a, Xq, amax, rinv);
+        case 1: return rms_rc<1, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
+        case 2: return rms_rc<2, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
+        case 3: return rms_rc<3, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
+        case 4: return rms_rc<4, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
+        case 6: return rms_rc<6, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
+        default: return rms_rc<8, ADD>(cfg, X, R, H, w, K, eps_n, eps_a, Xq, amax, rinv);
     }
+}
+
+cudaError_t launch_rmsnorm_quant(const void *X, const float *w, int64_t T, int64_t K, float eps_n, float eps_a,
+                                 int8_t *Xq, float *amax, float *rinv, cudaStream_t s) {
+    return rms_launch<false>(X, nullptr, nullptr, w, T, K, eps_n, eps_a, Xq, amax, rinv, s);
+}
+
+cudaError_t launch_add_rmsnorm_quant(const void *X, const void *R, const float *w, int64_t T, int64_t K, float eps_n,
+                                     float eps_a, void *H, int8_t *Xq, float *amax, float *rinv, cudaStream_t s) {
+    return rms_launch<true>(X, R, H, w, T, K, eps_n, eps_a, Xq, amax, rinv, s);
 }
 
 size_t swiglu_smem_bytes(int64_t F) { return static_cast<size_t>(F) * 4; }

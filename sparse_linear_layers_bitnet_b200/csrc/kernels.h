@@ -108,6 +108,8 @@ constexpr size_t kSwigluMaxSmem = 200 * 1024;   // h of one token row in fp32
 size_t swiglu_smem_bytes(int64_t F);
 cudaError_t launch_rmsnorm_quant(const void *X, const float *w, int64_t T, int64_t K, float eps_n, float eps_a,
                                  int8_t *Xq, float *amax, float *rinv, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_quant(const void *X, const void *R, const float *w, int64_t T, int64_t K, float eps_n,
+                                     float eps_a, void *H, int8_t *Xq, float *amax, float *rinv, cudaStream_t s);
 cudaError_t launch_swiglu_quant(const void *G, const void *U, int64_t ld, int64_t T, int64_t F, float eps_a,
                                 int8_t *Xq, float *amax, cudaStream_t s);
 

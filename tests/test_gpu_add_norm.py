@@ -1,0 +1,141 @@
+"""GPU parity of the residual addition fused with RMSNorm and the per-token
+quantisation: the new residual stream, codes, absmax and norm factor bit-exact
+against the oracle's rmsnorm and quant_act of bf16(X + R).
+
+"BitNet b1.58: Ternary Weights for 1.58-bit LLMs", "What this paper explains"
+(LLaMA-alike pre-norm blocks) and "The mechanism" (per-token absmax int8
+activations).
+"""
+import numpy as np
+import pytest
+
+import oracle
+from sparse_linear_layers_bitnet_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def bn(cuda_device):
+    import sparse_linear_layers_bitnet_b200 as m
+    m.load()
+    return m
+
+
+def bf16_dev(a_f32):
+    bits = synth.to_bf16_bits(a_f32)
+    return torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16), synth.bf16_bits_to_f32(bits)
+
+
+def _sum_bits(X, R):
+    """bf16 bits of the exact sum: fp64 holds every sum of two bf16 values whose
+    exponents are less than 45 apart, and further apart the larger one is the
+    rounded sum; fp64 to bf16 goes through fp32 rounded to odd, so that the
+    result is rounded once."""
+    s = X.astype(np.float64) + R.astype(np.float64)
+    f = s.astype(np.float32)
+    up = np.abs(f.astype(np.float64)) > np.abs(s)          # truncate towards zero, then set the sticky bit
+    u = f.view(np.uint32).copy()
+    u[up] -= 1
+    inexact = u.view(np.float32).astype(np.float64) != s
+    u[inexact] |= 1
+    return synth.to_bf16_bits(u.view(np.float32))
+
+
+def _rows(T, K, seed):
+    r = np.random.default_rng(seed)
+    X = r.normal(size=(T, K)).astype(np.float32)
+    R = (r.normal(size=(T, K)) * np.where(r.random(K) < 0.02, 20.0, 1.0)).astype(np.float32)
+    if T > 2:
+        R[1] = -X[1]                                        # the sum vanishes: absmax is the floor
+        X[2] *= np.float32(2.0) ** r.integers(-60, 60, K).astype(np.float32)     # far exponents, ties of the addition
+        R[2] *= np.float32(2.0) ** r.integers(-60, 60, K).astype(np.float32)
+    if T > 4:
+        X[3] *= 1e-30
+        R[3] *= 1e-38                                       # subnormal summands
+        X[4, ::2] = 0.0
+        R[4] = 0.0
+    return X, R
+
+
+@pytest.mark.parametrize("T,K,weighted", [(1, 8, False), (1, 2560, True), (7, 264, True), (33, 3200, True), (5, 4096, False),
+                                          (6, 8640, True), (5, 16384, True), (5, 20000, True), (5, 65536, False)])
+def test_add_rmsnorm_quant_matches_the_oracle(bn, T, K, weighted):
+    Xf, Rf = _rows(T, K, T * 7 + K)
+    Xd, X = bf16_dev(Xf)
+    Rd, R = bf16_dev(Rf)
+    w = (1 + 0.1 * np.random.default_rng(K).normal(size=K)).astype(np.float32) if weighted else None
+    wd = torch.from_numpy(w).cuda() if weighted else None
+    Hb = _sum_bits(X, R)
+    Hf = synth.bf16_bits_to_f32(Hb)
+    xn, r = oracle.rmsnorm(Hf, 1e-6, w, return_r=True)
+    q, a = oracle.quant_act(xn, 1e-5)
+    H, Xq, am, rinv = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=wd)
+    torch.cuda.synchronize()
+    assert np.array_equal(H.view(torch.int16).cpu().numpy().view(np.uint16), Hb)
+    assert np.array_equal(rinv.cpu().numpy(), r)
+    assert np.array_equal(am.cpu().numpy(), a)
+    assert np.array_equal(Xq.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("K", [512, 3200, 24576])
+@pytest.mark.parametrize("into", ["X", "R"])
+def test_the_sum_may_go_into_an_input(bn, K, into):
+    Xd, _ = bf16_dev(synth.activations(9, K, seed=K))
+    Rd, _ = bf16_dev(synth.activations(9, K, seed=K + 1, outlier_p=0.01))
+    ref = bn.bitnet_add_rmsnorm_quant(Xd, Rd)
+    other = Rd.clone() if into == "X" else Xd.clone()
+    got = bn.bitnet_add_rmsnorm_quant(Xd, Rd, H=Xd if into == "X" else Rd)
+    torch.cuda.synchronize()
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+    assert torch.equal(Rd if into == "X" else Xd, other)
+
+
+@pytest.mark.parametrize("K", [2560, 16392])
+def test_a_weight_off_16_bytes_gives_the_same(bn, K):
+    Xd, _ = bf16_dev(synth.activations(4, K, seed=1))
+    Rd, _ = bf16_dev(synth.activations(4, K, seed=2))
+    w = torch.rand(K + 1, device="cuda") + 0.5
+    ref = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=w[1:].clone())
+    got = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=w[1:])
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_same_as_rmsnorm_quant_of_the_sum(bn):
+    Xd, _ = bf16_dev(synth.activations(300, 3200, seed=3))
+    Rd, _ = bf16_dev(synth.activations(300, 3200, seed=4, outlier_p=0.01))
+    w = torch.rand(3200, device="cuda") + 0.5
+    H, Xq, am, rinv = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=w)
+    r2 = torch.empty(300, device="cuda")
+    Xq2, am2 = bn.bitnet_rmsnorm_quant(H, w, rinv=r2)
+    assert torch.equal(H, Xd + Rd)
+    assert torch.equal(Xq, Xq2) and torch.equal(am, am2) and torch.equal(rinv, r2)
+
+
+def test_empty_batch_and_another_stream(bn):
+    e = torch.empty((0, 512), dtype=torch.bfloat16, device="cuda")
+    assert bn.bitnet_add_rmsnorm_quant(e, e)[1].shape == (0, 512)
+    Xd, _ = bf16_dev(synth.activations(64, 2560, seed=5))
+    Rd, _ = bf16_dev(synth.activations(64, 2560, seed=6))
+    ref = bn.bitnet_add_rmsnorm_quant(Xd, Rd)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = bn.bitnet_add_rmsnorm_quant(Xd, Rd, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_refusals(bn):
+    X = torch.zeros((4, 512), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(AssertionError):
+        bn.bitnet_add_rmsnorm_quant(X, X[:2])
+    with pytest.raises(AssertionError):
+        bn.bitnet_add_rmsnorm_quant(X.float(), X)
+    with pytest.raises(AssertionError):
+        bn.bitnet_add_rmsnorm_quant(X, X, w=torch.ones(512, device="cuda", dtype=torch.bfloat16))
+    buf = torch.zeros((6, 512), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(bn.BitnetError):   # overlaps X by two rows
+        bn.bitnet_add_rmsnorm_quant(buf[:4], X, H=buf[2:])
