@@ -367,6 +367,39 @@ bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float
                                        bitnet_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * bitnet_rmsnorm_grad - gradient of RMSNorm with its residual branch.
+ *
+ * "Sparse-BitNet" (gist.science), section 2 "Training Strategie": gradients
+ * pass straight through the quantisers, so the gradient dY that an input
+ * gradient product (bitnet_dgrad) leaves at the int8 codes is the gradient at
+ * the normalised values y_k = h_k r w_k.  Per token, with e_k = dY_k w_k and
+ * u_k = h_k r:
+ *   dH_k = r (e_k - u_k (1/K) sum_j e_j u_j) + dR_k;
+ *   dw_k = sum_t dY[t,k] u[t,k].
+ * dR is the gradient that reaches the same residual stream from above; as
+ * h = x + r, dH is the gradient of both summands of bitnet_add_rmsnorm_quant.
+ * Sums are fp32, in an order that depends on the sizes and the device only;
+ * dH is rounded once.
+ *
+ *   dY        [T, K] of dy_dtype (fp32 or bf16).   H  [T, K] bf16, the normed rows.
+ *   w         [K] fp32 norm weight or NULL (no weight).
+ *   rinv      [T] fp32: r, as the forward wrote it.
+ *   dR        [T, K] of g_dtype or NULL (no residual branch).
+ *   dH        [T, K] of g_dtype out; may be dR itself, no other overlap.
+ *   dw        [K] fp32 out or NULL; accumulate != 0 adds to it (gradient
+ *             accumulation), else it is overwritten (T = 0: zeros).
+ *   ws        >= bitnet_rmsnorm_grad_workspace_size(T, K) bytes, 16-byte aligned,
+ *             contents ignored; may be NULL when dw is NULL.
+ * dY, H, w, dR and dH 16-byte aligned; K % 8 == 0, K <= 65536.
+ * Errors: INVALID_ARG, UNSUPPORTED (T >= 2^31), WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------ */
+size_t bitnet_rmsnorm_grad_workspace_size(int64_t T, int64_t K);
+bitnet_status bitnet_rmsnorm_grad(const void *dY, bitnet_dtype dy_dtype, const void *H, const float *w,
+                                  const float *rinv, const void *dR, bitnet_dtype g_dtype, int64_t T, int64_t K,
+                                  void *dH, float *dw, int32_t accumulate, void *ws, size_t ws_bytes,
+                                  bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * bitnet_swiglu_quant - SwiGLU gate fused into the per-token quantisation.
  *
  * Same pages and sections as bitnet_rmsnorm_quant.  Per token t and column f:

@@ -29,7 +29,8 @@ EXPORTED = [
     "bitnet_pack_update_workspace_size", "bitnet_pack_nm_update",
     "bitnet_pack_update_batch_workspace_size", "bitnet_pack_nm_update_batch",
     "bitnet_pack_6of8_windows", "bitnet_quant_act_lift_6of8",
-    "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_add_rmsnorm_quant", "bitnet_swiglu_quant",
+    "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_add_rmsnorm_quant",
+    "bitnet_rmsnorm_grad_workspace_size", "bitnet_rmsnorm_grad", "bitnet_swiglu_quant",
     "bitnet_linear_workspace_size", "bitnet_sparse_linear",
     "bitnet_quant_linear_workspace_size", "bitnet_quant_linear",
     "bitnet_decode_chain_workspace_size", "bitnet_decode_chain",
@@ -120,6 +121,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "bitnet_quant_act": (I32, [P, I32, I64, I64, F, P, P, P]),
         "bitnet_rmsnorm_quant": (I32, [P, P, I64, I64, F, F, P, P, P, P]),
         "bitnet_add_rmsnorm_quant": (I32, [P, P, P, I64, I64, F, F, P, P, P, P, P]),
+        "bitnet_rmsnorm_grad_workspace_size": (SZ, [I64, I64]),
+        "bitnet_rmsnorm_grad": (I32, [P, I32, P, P, P, P, I32, I64, I64, P, P, I32, P, SZ, P]),
         "bitnet_swiglu_quant": (I32, [P, P, I64, I64, I64, F, P, P, P]),
         "bitnet_linear_workspace_size": (SZ, []),
         "bitnet_sparse_linear": (I32, [P, P, ctypes.POINTER(BitnetPackedW), I64, P, I32, P, P, SZ, P]),
@@ -194,6 +197,16 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _ws(ws, nbytes, like, stream):
+    """(tensor that holds it, address, size) of the workspace ws, or of one for this call."""
+    if ws is not None:
+        assert ws.buf.device == like.device
+        return ws.buf, ws.buf.data_ptr(), ws.nbytes
+    torch = _torch()
+    buf = _new((int(max(nbytes, 256)),), torch.uint8, like, stream)
+    return buf, buf.data_ptr(), buf.numel()
 
 
 def _addr(t):
@@ -478,6 +491,28 @@ def bitnet_add_rmsnorm_quant(X, R, w=None, eps_norm: float = 1e-6, eps_act: floa
     _launch("bitnet_add_rmsnorm_quant", X, stream, X.data_ptr(), R.data_ptr(), _addr(w), T, K, eps_norm, eps_act,
             H.data_ptr(), Xq.data_ptr(), absmax.data_ptr(), rinv.data_ptr())
     return H, Xq, absmax, rinv
+
+
+def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumulate: bool = False,
+                        ws: "Workspace | None" = None, stream=None):
+    """Gradient of RMSNorm at its rows H (bf16 [T, K], rinv as the forward wrote it) for the gradient dY
+    (fp32 or bf16) of the normalised values; dR: the residual stream's own gradient, added to dH.
+    Returns (dH, dw): dH of dR's (or dH's own) type, bf16 unless given; dw fp32."""
+    torch = _torch()
+    lib = load()
+    T, K = H.shape
+    assert _is(H, torch.bfloat16, (T, K), H) and H.is_cuda and _is(rinv, torch.float32, (T,), H)
+    assert dY.dtype in (torch.float32, torch.bfloat16) and _is(dY, dY.dtype, (T, K), H)
+    assert _is(w, torch.float32, (K,), H, optional=True)
+    g = dH.dtype if dH is not None else dR.dtype if dR is not None else torch.bfloat16
+    dH = _new((T, K), g, H, stream) if dH is None else dH
+    dw = _new((K,), torch.float32, H, stream) if dw is None else dw
+    assert _is(dR, g, (T, K), H, optional=True) and _is(dH, g, (T, K), H) and _is(dw, torch.float32, (K,), H)
+    keep, ws_ptr, ws_bytes = _ws(ws, lib.bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
+    _launch("bitnet_rmsnorm_grad", H, stream, dY.data_ptr(), _dtype_code(dY.dtype), H.data_ptr(), _addr(w),
+            rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
+            ws_ptr, ws_bytes)
+    return dH, dw
 
 
 def bitnet_swiglu_quant(GU, F: int | None = None, eps_act: float = 1e-5, Xq=None, absmax=None, stream=None):

@@ -357,6 +357,41 @@ bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float
                        "add_rmsnorm_quant");
 }
 
+size_t bitnet_rmsnorm_grad_workspace_size(int64_t T, int64_t K) { return bitnet::rmsnorm_grad_ws_bytes(T, K); }
+
+bitnet_status bitnet_rmsnorm_grad(const void *dY, bitnet_dtype dy_dtype, const void *H, const float *w,
+                                  const float *rinv, const void *dR, bitnet_dtype g_dtype, int64_t T, int64_t K,
+                                  void *dH, float *dw, int32_t accumulate, void *ws, size_t ws_bytes,
+                                  bitnet_stream_t stream) {
+    if (T < 0 || K <= 0 || K % 8 || K > 65536) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: need T >= 0, 0 < K <= 65536, K %% 8 == 0");
+    if (dy_dtype != BITNET_F32 && dy_dtype != BITNET_BF16) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: bad dY dtype");
+    if (g_dtype != BITNET_F32 && g_dtype != BITNET_BF16) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: bad gradient dtype");
+    if (dw && !aligned(dw, 4)) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: dw must be 4-byte aligned");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) {   // an empty sum: dw = 0, or unchanged when accumulating
+        if (!dw || accumulate) return BITNET_OK;
+        return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(K) * 4, s), "rmsnorm_grad");
+    }
+    if (!dY || !H || !rinv || !dH) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: null pointer");
+    if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(dH, 16) || !aligned(dR, 16) || !aligned(w, 16))
+        return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: dY, H, w, dR and dH must be 16-byte aligned");
+    if (T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "rmsnorm_grad: T too large");
+    if (dw) {
+        if (!ws) return fail(BITNET_ERR_WORKSPACE, "rmsnorm_grad: dw needs a workspace");
+        if (ws_bytes < bitnet_rmsnorm_grad_workspace_size(T, K))
+            return fail(BITNET_ERR_WORKSPACE, "rmsnorm_grad: workspace needs %zu bytes", bitnet_rmsnorm_grad_workspace_size(T, K));
+        if (!aligned(ws, 16)) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: ws must be 16-byte aligned");
+    }
+    const size_t n = static_cast<size_t>(T) * static_cast<size_t>(K);
+    const size_t gb = n * (g_dtype == BITNET_F32 ? 4 : 2);
+    if ((dR && dR != dH && overlaps(dH, gb, dR, gb)) || overlaps(dH, gb, H, n * 2) ||
+        overlaps(dH, gb, dY, n * (dy_dtype == BITNET_F32 ? 4 : 2)))
+        return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: dH may be dR, no other overlap is allowed");
+    return cuda_status(bitnet::launch_rmsnorm_grad(dY, dy_dtype == BITNET_BF16, H, w, rinv, dR, g_dtype == BITNET_BF16, T, K,
+                                                   dH, dw, accumulate != 0, ws, s),
+                       "rmsnorm_grad");
+}
+
 bitnet_status bitnet_swiglu_quant(const void *G, const void *U, int64_t ld, int64_t T, int64_t F, float eps_act,
                                   int8_t *Xq, float *absmax, bitnet_stream_t stream) {
     if (T < 0 || F <= 0 || F % 8 || ld < F) return fail(BITNET_ERR_INVALID_ARG, "swiglu_quant: need T >= 0, F > 0, F %% 8 == 0, ld >= F");

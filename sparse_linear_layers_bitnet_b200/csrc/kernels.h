@@ -113,6 +113,12 @@ cudaError_t launch_add_rmsnorm_quant(const void *X, const void *R, const float *
 cudaError_t launch_swiglu_quant(const void *G, const void *U, int64_t ld, int64_t T, int64_t F, float eps_a,
                                 int8_t *Xq, float *amax, cudaStream_t s);
 
+// Gradient of the (residual +) RMSNorm step (norm_grad.cu)
+size_t rmsnorm_grad_ws_bytes(int64_t T, int64_t K);
+cudaError_t launch_rmsnorm_grad(const void *dY, bool dy_bf16, const void *H, const float *w, const float *rinv,
+                                const void *dR, bool g_bf16, int64_t T, int64_t K, void *dH, float *dw, bool accumulate,
+                                void *ws, cudaStream_t s);
+
 cudaError_t launch_gemv_dec(const int8_t *Xq, const float *amax, const float *gamma, const uint8_t *dec,
                             int64_t T, int64_t n_out, int64_t k, void *Y, bool y_bf16, int32_t *acc,
                             cudaStream_t s);

@@ -48,3 +48,27 @@ def test_add_rmsnorm_quant_refusals(lib):
     assert call(f, ok, Xq=at(4)) == INVALID
     assert b"overlap" in lib.bitnet_last_error()
     assert call(f, ok, T=0, X=None, R=None, H=None, Xq=None, absmax=None) == _abi.BITNET_OK
+
+
+def test_rmsnorm_grad_refusals(lib):
+    f = lib.bitnet_rmsnorm_grad
+    ok = dict(dY=at(1), dy_dtype=1, H=at(2), w=at(3), rinv=at(4), dR=at(5), g_dtype=1, T=4, K=512, dH=at(6), dw=at(7),
+              accumulate=0, ws=at(8), ws_bytes=1 << 30, stream=None)
+    for name in ("dY", "H", "rinv", "dH"):
+        assert call(f, ok, **{name: None}) == INVALID, name
+    for name in ("dY", "H", "w", "dR", "dH", "ws"):
+        assert call(f, ok, **{name: ok[name] + 8}) == INVALID, name
+    for name in ("dy_dtype", "g_dtype"):
+        assert call(f, ok, **{name: 2}) == INVALID
+    for K in (0, 12, 65544):
+        assert call(f, ok, K=K) == INVALID
+    assert call(f, ok, T=-1) == INVALID
+    assert call(f, ok, T=1 << 31) == UNSUPPORTED
+    assert call(f, ok, ws=None) == WORKSPACE
+    assert call(f, ok, ws_bytes=lib.bitnet_rmsnorm_grad_workspace_size(4, 512) - 1) == WORKSPACE
+    assert call(f, ok, dH=at(1)) == INVALID       # over dY
+    assert call(f, ok, dH=at(2, 16)) == INVALID   # over H
+    assert call(f, ok, dH=at(5, 16)) == INVALID   # over a part of dR
+    assert b"overlap" in lib.bitnet_last_error()
+    assert call(f, ok, T=0, dw=None) == _abi.BITNET_OK
+    assert lib.bitnet_rmsnorm_grad_workspace_size(1, 512) >= 512 * 4
