@@ -400,6 +400,90 @@ bitnet_status bitnet_rmsnorm_grad(const void *dY, bitnet_dtype dy_dtype, const v
                                   bitnet_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * bitnet_rope - rotary positions on the heads of a row, or their inverse.
+ *
+ * "BitNet b1.58 ...", section "What this paper explains": the blocks around
+ * BitLinear are LLaMA-alike, which turn each pair (a, b) of a query's or key's
+ * features by the angle of its position.  With (c, s) of the row's position
+ * and the pair's frequency from the table:
+ *   a' = fp32(fp32(a c) - fp32(b s));   b' = fp32(fp32(b c) + fp32(a s)),
+ * then one rounding to the type of Y.  inverse != 0 takes -s: the rotation is
+ * orthogonal, so this is the gradient.
+ *
+ *   X         [T, ldx] fp32 or bf16; heads 0 .. n_heads-1 of a row lie at
+ *             h * head_dim (the query and key heads of a QKV row, for example).
+ *   pos       [T] int32 positions; a negative one marks a padding row, whose Y
+ *             is left as it was.
+ *   table     [n_pos, rot_dim / 2, 2] fp32: cos and sin of every position and
+ *             frequency (any scaling for long contexts is in it), 8-byte
+ *             aligned; may be NULL when rot_dim is 0.
+ *   head_dim  1 .. 256; rot_dim: even, <= head_dim: the features behind it are
+ *             copied.
+ *   layout    BITNET_ROPE_HALVES: pair i is (x_i, x_{i + rot_dim/2});
+ *             BITNET_ROPE_INTERLEAVED: pair i is (x_{2i}, x_{2i+1}).
+ *   Y         [T, ldy] of the same type; may be X itself with ldy == ldx.
+ *   ws        >= bitnet_rope_workspace_size() bytes, 16-byte aligned: the status
+ *             word.  A position >= n_pos sets it (bitnet_read_device_status
+ *             returns INVALID_ARG) and leaves that row of Y as it was.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------ */
+enum { BITNET_ROPE_HALVES = 0, BITNET_ROPE_INTERLEAVED = 1 };
+
+size_t bitnet_rope_workspace_size(void);
+bitnet_status bitnet_rope(const void *X, bitnet_dtype dtype, int64_t ldx, const int32_t *pos, const float *table,
+                          int64_t n_pos, int64_t T, int64_t n_heads, int64_t head_dim, int64_t rot_dim, int32_t layout,
+                          int32_t inverse, void *Y, int64_t ldy, void *ws, size_t ws_bytes, bitnet_stream_t stream);
+
+/*
+ * A paged key-value cache in bf16: key j of a sequence lies in row
+ * j % page_size of the page that its page list names at j / page_size, at
+ * page * page_stride + head * head_stride + row * row_stride (elements).  The
+ * strides are multiples of 8, at least head_dim, and the head_dim elements
+ * rounded up to a multiple of 8 of every row must be readable (what lies
+ * behind head_dim is not used).  k and v 16-byte aligned device pointers;
+ * page_size a power of two, 8 .. 65536; head_dim <= 256.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t n_pages;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t row_stride;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} bitnet_kv_cache;
+
+/* ------------------------------------------------------------------------
+ * bitnet_rope_append - rotary positions on a QKV product's rows, with the keys
+ * and values written into a paged cache.
+ *
+ * Row t holds n_heads query heads, n_kv_heads key heads and n_kv_heads value
+ * heads.  The query and key heads are turned as in bitnet_rope and rounded to
+ * bf16; the query heads go to Q, the key heads and the value heads (rounded to
+ * bf16, not turned) to row pos[t] of sequence seq[t] in the cache.
+ *
+ *   QKV       [T, ld] fp32 or bf16.
+ *   pos       [T] int32: the row's position, which is also its place in its
+ *             sequence's cache.   seq  [T] int32 sequence of each row, or NULL
+ *             (row t belongs to sequence t).  A negative pos or seq marks a
+ *             padding row: nothing is written for it.  No two rows may have the
+ *             same (seq, pos).
+ *   table, n_pos, rot_dim, layout   as bitnet_rope (rot_dim = 0: no rotation).
+ *   cache     host struct, read during the call only.
+ *   pages     [n_seqs, max_pages] int32: every sequence's pages in order.
+ *   Q         [T, n_heads * head_dim] bf16 out.
+ *   ws        as bitnet_rope; a position, sequence or page out of range sets the
+ *             status word, and nothing is written for its row.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------ */
+bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld, const int32_t *pos, const int32_t *seq,
+                                 const float *table, int64_t n_pos, int64_t T, int64_t n_heads, int64_t rot_dim,
+                                 int32_t layout, const bitnet_kv_cache *cache, const int32_t *pages, int64_t n_seqs,
+                                 int64_t max_pages, void *Q, void *ws, size_t ws_bytes, bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * bitnet_swiglu_quant - SwiGLU gate fused into the per-token quantisation.
  *
  * Same pages and sections as bitnet_rmsnorm_quant.  Per token t and column f:
@@ -626,8 +710,9 @@ bitnet_status bitnet_tensor_peak(int32_t kind, int64_t iters, double *ops, void 
 /* ------------------------------------------------------------------------
  * Status helpers.
  * bitnet_read_device_status synchronises `stream`, reads the status word that
- * the kernels of the last call on `ws` left (BITNET_OK or BITNET_ERR_TIMEOUT
- * when a bounded wait gave up) and clears it.
+ * the kernels of the calls on `ws` left (BITNET_OK, BITNET_ERR_TIMEOUT when a
+ * bounded wait gave up, or BITNET_ERR_INVALID_ARG when a kernel met an index on
+ * the device that is out of range) and clears it.
  * ------------------------------------------------------------------------ */
 bitnet_status bitnet_read_device_status(void *ws, bitnet_stream_t stream);
 const char *bitnet_status_string(bitnet_status s);

@@ -30,7 +30,8 @@ EXPORTED = [
     "bitnet_pack_update_batch_workspace_size", "bitnet_pack_nm_update_batch",
     "bitnet_pack_6of8_windows", "bitnet_quant_act_lift_6of8",
     "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_add_rmsnorm_quant",
-    "bitnet_rmsnorm_grad_workspace_size", "bitnet_rmsnorm_grad", "bitnet_swiglu_quant",
+    "bitnet_rmsnorm_grad_workspace_size", "bitnet_rmsnorm_grad",
+    "bitnet_rope_workspace_size", "bitnet_rope", "bitnet_rope_append", "bitnet_swiglu_quant",
     "bitnet_linear_workspace_size", "bitnet_sparse_linear",
     "bitnet_quant_linear_workspace_size", "bitnet_quant_linear",
     "bitnet_decode_chain_workspace_size", "bitnet_decode_chain",
@@ -87,6 +88,20 @@ class BitnetChainOp(ctypes.Structure):
     ]
 
 
+class BitnetKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
 class BitnetError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         super().__init__(f"{where}: status {status} ({detail})")
@@ -123,6 +138,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "bitnet_add_rmsnorm_quant": (I32, [P, P, P, I64, I64, F, F, P, P, P, P, P]),
         "bitnet_rmsnorm_grad_workspace_size": (SZ, [I64, I64]),
         "bitnet_rmsnorm_grad": (I32, [P, I32, P, P, P, P, I32, I64, I64, P, P, I32, P, SZ, P]),
+        "bitnet_rope_workspace_size": (SZ, []),
+        "bitnet_rope": (I32, [P, I32, I64, P, P, I64, I64, I64, I64, I64, I32, I32, P, I64, P, SZ, P]),
+        "bitnet_rope_append": (I32, [P, I32, I64, P, P, P, I64, I64, I64, I64, I32, ctypes.POINTER(BitnetKvCache), P, I64,
+                                     I64, P, P, SZ, P]),
         "bitnet_swiglu_quant": (I32, [P, P, I64, I64, I64, F, P, P, P]),
         "bitnet_linear_workspace_size": (SZ, []),
         "bitnet_sparse_linear": (I32, [P, P, ctypes.POINTER(BitnetPackedW), I64, P, I32, P, P, SZ, P]),
@@ -200,13 +219,19 @@ def _new(shape, dtype, like, stream):
 
 
 def _ws(ws, nbytes, like, stream):
-    """(tensor that holds it, address, size) of the workspace ws, or of one for this call."""
+    """(tensor that holds it, address, size) of the workspace ws, or of one for this call
+    (whose status word nobody reads)."""
     if ws is not None:
         assert ws.buf.device == like.device
         return ws.buf, ws.buf.data_ptr(), ws.nbytes
     torch = _torch()
     buf = _new((int(max(nbytes, 256)),), torch.uint8, like, stream)
     return buf, buf.data_ptr(), buf.numel()
+
+
+def _ld(t) -> int:
+    """Row stride of a matrix (a single row has none of its own: its width)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _addr(t):
@@ -513,6 +538,110 @@ def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumula
             rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
             ws_ptr, ws_bytes)
     return dH, dw
+
+
+def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda"):
+    """The table of bitnet_rope, [n_pos, rot_dim / 2, 2] fp32: cos and sin of position p times
+    frequency f_i = base^(-2i / rot_dim), angles and functions in 64 bits.  Made once, before a run.
+
+    scaling, for contexts longer than a model was trained on:
+      {"type": "linear", "factor": s}: f_i / s;
+      {"type": "base", "factor": s}: base * s^(rot_dim / (rot_dim - 2)), so that the
+        lowest frequency is divided by s and the highest kept;
+      {"type": "parts", "factor": s, "original": L, "fast": 32, "slow": 1, "amplitude": 0.1 ln s + 1}:
+        frequencies that make more than `fast` turns over the L original positions are
+        kept, those with fewer than `slow` divided by s, a linear ramp in the turns
+        between; cos and sin times the amplitude.
+    """
+    import math
+    torch = _torch()
+    assert n_pos > 0 and rot_dim > 0 and rot_dim % 2 == 0
+    amplitude, kind = 1.0, None
+    if scaling is not None:
+        kind, s = scaling["type"], float(scaling["factor"])
+        assert kind in ("linear", "base", "parts") and s >= 1.0
+    if kind == "base" and rot_dim > 2:
+        base = base * s ** (rot_dim / (rot_dim - 2))
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    if kind == "linear":
+        f = f / s
+    elif kind == "parts":
+        fast, slow = float(scaling.get("fast", 32)), float(scaling.get("slow", 1))
+        keep = ((scaling["original"] * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / s)
+        amplitude = float(scaling.get("amplitude", 0.1 * math.log(s) + 1.0))
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.stack((a.cos(), a.sin()), dim=-1) * amplitude).to(torch.float32)
+
+
+def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """Keys or values of a paged cache, bf16 [n_pages, n_kv_heads, page_size, head_dim], zeros; rows lie
+    on 16 bytes (a head_dim that is not a multiple of 8 gets a longer row stride)."""
+    torch = _torch()
+    ld = -(-head_dim // 8) * 8
+    return torch.zeros((n_pages, n_kv_heads, page_size, ld), dtype=torch.bfloat16, device=device)[..., :head_dim]
+
+
+def _cache_struct(K, V) -> BitnetKvCache:
+    torch = _torch()
+    assert K.dim() == 4 and K.dtype == V.dtype == torch.bfloat16 and K.is_cuda and K.device == V.device
+    n_pages, kv, page, d = K.shape
+    assert V.shape == K.shape and (d == 1 or K.stride(3) == V.stride(3) == 1)
+    # the stride of an axis of one says nothing: any valid one
+    (sp, sh, sr), other = ([st if n > 1 else -(-d // 8) * 8 for n, st in zip(t.shape[:3], t.stride())] for t in (K, V))
+    assert [sp, sh, sr] == other
+    return BitnetKvCache(K.data_ptr(), V.data_ptr(), n_pages, sp, sh, sr, page, kv, d)
+
+
+def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interleaved: bool = False,
+                inverse: bool = False, Y=None, ws: "Workspace | None" = None, stream=None):
+    """Rotary positions pos (int32 [T]) on the first n_heads heads of the rows of X (fp32 or bf16
+    [T, >= n_heads * head_dim], rows may be strided); table as rope_table makes it.  inverse: the
+    gradient.  Y may be X.  Returns Y."""
+    torch = _torch()
+    assert X.dim() == 2 and X.dtype in (torch.float32, torch.bfloat16) and X.is_cuda and (X.shape[1] == 0 or X.stride(1) == 1)
+    T = X.shape[0]
+    if head_dim is None:
+        head_dim = X.shape[1] // n_heads
+    assert X.shape[1] >= n_heads * head_dim
+    assert _is(pos, torch.int32, (T,), X)
+    n_pos, half, two = table.shape
+    assert two == 2 and _is(table, torch.float32, (n_pos, half, 2), X)
+    if Y is None:
+        Y = _new((T, n_heads * head_dim), X.dtype, X, stream)
+    assert Y.dim() == 2 and Y.dtype == X.dtype and Y.device == X.device and Y.stride(1) == 1
+    assert Y.shape[0] == T and Y.shape[1] >= n_heads * head_dim
+    keep, ws_ptr, ws_bytes = _ws(ws, 256, X, stream)
+    _launch("bitnet_rope", X, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(), table.data_ptr(), n_pos,
+            T, n_heads, head_dim, 2 * half, 1 if interleaved else 0, 1 if inverse else 0, Y.data_ptr(), _ld(Y), ws_ptr,
+            ws_bytes)
+    return Y
+
+
+def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool = False, Q=None,
+                       ws: "Workspace | None" = None, stream=None):
+    """Rotary positions on the query and key heads of QKV (fp32 or bf16 [T, (heads + 2 kv heads) * head_dim],
+    rows may be strided); keys and values go to the cache K, V (bf16 [pages, kv heads, page, head_dim], any
+    strides with contiguous rows), row pos of sequence seq (default: row t is sequence t) by its page list in
+    pages (int32 [sequences, most pages]).  table None: no rotation.  Returns Q (bf16 [T, heads * head_dim])."""
+    torch = _torch()
+    c = _cache_struct(K, V)
+    assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1 and QKV.device == K.device
+    T, width = QKV.shape
+    heads = width // c.head_dim - 2 * c.n_kv_heads
+    assert heads > 0 and width == (heads + 2 * c.n_kv_heads) * c.head_dim
+    assert _is(pos, torch.int32, (T,), QKV) and _is(seq, torch.int32, (T,), QKV, optional=True)
+    n_seqs, max_pages = pages.shape
+    assert _is(pages, torch.int32, (n_seqs, max_pages), QKV)
+    n_pos, half = (table.shape[0], table.shape[1]) if table is not None else (0, 0)
+    assert _is(table, torch.float32, (n_pos, half, 2), QKV, optional=True)
+    Q = _new((T, heads * c.head_dim), torch.bfloat16, QKV, stream) if Q is None else Q
+    assert _is(Q, torch.bfloat16, (T, heads * c.head_dim), QKV)
+    keep, ws_ptr, ws_bytes = _ws(ws, 256, QKV, stream)
+    _launch("bitnet_rope_append", QKV, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV), pos.data_ptr(), _addr(seq),
+            _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0, ctypes.byref(c), pages.data_ptr(), n_seqs,
+            max_pages, Q.data_ptr(), ws_ptr, ws_bytes)
+    return Q
 
 
 def bitnet_swiglu_quant(GU, F: int | None = None, eps_act: float = 1e-5, Xq=None, absmax=None, stream=None):

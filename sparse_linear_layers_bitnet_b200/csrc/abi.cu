@@ -406,6 +406,104 @@ bitnet_status bitnet_swiglu_quant(const void *G, const void *U, int64_t ld, int6
                        "swiglu_quant");
 }
 
+// the checks of a key-value cache's description that every entry point with one makes
+static bitnet_status kv_cache_check(const char *who, const bitnet_kv_cache *c, bitnet::KvCacheHost *out) {
+    if (!c || !c->k || !c->v) return fail(BITNET_ERR_INVALID_ARG, "%s: the cache with its k and v is required", who);
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(BITNET_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned", who);
+    if (c->n_pages < 1 || c->n_kv_heads < 1 || c->head_dim < 1 || c->page_size < 1)
+        return fail(BITNET_ERR_INVALID_ARG, "%s: the cache's sizes must be positive", who);
+    if (c->n_pages > 2147483647LL || c->n_kv_heads > 65535) return fail(BITNET_ERR_UNSUPPORTED, "%s: too many pages or heads", who);
+    if (c->head_dim > 256) return fail(BITNET_ERR_UNSUPPORTED, "%s: head_dim > 256", who);
+    if (c->page_size < 8 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)))
+        return fail(BITNET_ERR_UNSUPPORTED, "%s: page_size must be a power of two from 8 to 65536", who);
+    for (int64_t st : {c->page_stride, c->head_stride, c->row_stride})
+        if (st % 8 || st < c->head_dim)
+            return fail(BITNET_ERR_INVALID_ARG, "%s: the cache's strides must be multiples of 8 and at least head_dim", who);
+    int shift = 0;
+    while ((1 << shift) < c->page_size) ++shift;
+    *out = {c->k, c->v, c->n_pages, c->page_stride, c->head_stride, c->row_stride, shift, c->n_kv_heads, c->head_dim};
+    return BITNET_OK;
+}
+
+static bitnet_status rope_table_check(const char *who, const float *table, int64_t n_pos, int64_t rot_dim, int64_t head_dim,
+                                      int32_t layout) {
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
+        return fail(BITNET_ERR_INVALID_ARG, "%s: rot_dim must be even and at most head_dim", who);
+    if (layout != BITNET_ROPE_HALVES && layout != BITNET_ROPE_INTERLEAVED) return fail(BITNET_ERR_INVALID_ARG, "%s: bad layout", who);
+    if (rot_dim > 0 && (!table || n_pos < 1)) return fail(BITNET_ERR_INVALID_ARG, "%s: the table is required", who);
+    if (!aligned(table, 8)) return fail(BITNET_ERR_INVALID_ARG, "%s: the table must be 8-byte aligned", who);
+    return BITNET_OK;
+}
+
+static bitnet_status status_ws_check(const char *who, const void *ws, size_t ws_bytes) {
+    if (!ws) return fail(BITNET_ERR_WORKSPACE, "%s: workspace is required", who);
+    if (ws_bytes < bitnet::kLinearWsBytes) return fail(BITNET_ERR_WORKSPACE, "%s: workspace needs %zu bytes", who, bitnet::kLinearWsBytes);
+    if (!aligned(ws, 16)) return fail(BITNET_ERR_INVALID_ARG, "%s: ws must be 16-byte aligned", who);
+    return BITNET_OK;
+}
+
+size_t bitnet_rope_workspace_size(void) { return bitnet::kLinearWsBytes; }
+
+bitnet_status bitnet_rope(const void *X, bitnet_dtype dtype, int64_t ldx, const int32_t *pos, const float *table,
+                          int64_t n_pos, int64_t T, int64_t n_heads, int64_t head_dim, int64_t rot_dim, int32_t layout,
+                          int32_t inverse, void *Y, int64_t ldy, void *ws, size_t ws_bytes, bitnet_stream_t stream) {
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16) return fail(BITNET_ERR_INVALID_ARG, "rope: bad dtype");
+    if (T < 0 || n_heads < 1 || head_dim < 1) return fail(BITNET_ERR_INVALID_ARG, "rope: bad sizes");
+    if (n_heads > 65535 || head_dim > 256 || T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "rope: T, n_heads or head_dim too large");
+    if (ldx < n_heads * head_dim || ldy < n_heads * head_dim) return fail(BITNET_ERR_INVALID_ARG, "rope: a row holds n_heads * head_dim elements");
+    bitnet_status st = rope_table_check("rope", table, n_pos, rot_dim, head_dim, layout);
+    if (st != BITNET_OK) return st;
+    st = status_ws_check("rope", ws, ws_bytes);
+    if (st != BITNET_OK) return st;
+    if (T == 0) return BITNET_OK;   // an empty batch needs no buffers
+    if (!X || !Y || !pos) return fail(BITNET_ERR_INVALID_ARG, "rope: null pointer");
+    const size_t es = dtype == BITNET_F32 ? 4 : 2;
+    if (!aligned(X, es) || !aligned(Y, es) || !aligned(pos, 4)) return fail(BITNET_ERR_INVALID_ARG, "rope: X, Y or pos is not aligned to its elements");
+    const size_t row = static_cast<size_t>(n_heads * head_dim);
+    const size_t xb = (static_cast<size_t>(T - 1) * static_cast<size_t>(ldx) + row) * es;
+    const size_t yb = (static_cast<size_t>(T - 1) * static_cast<size_t>(ldy) + row) * es;
+    if (!(X == Y && ldx == ldy) && overlaps(X, xb, Y, yb))
+        return fail(BITNET_ERR_INVALID_ARG, "rope: Y may be X with the same stride, no other overlap is allowed");
+    return cuda_status(bitnet::launch_rope(X, dtype == BITNET_BF16, ldx, pos, table, n_pos, T, n_heads, head_dim, rot_dim,
+                                           layout == BITNET_ROPE_INTERLEAVED, inverse != 0, Y, ldy,
+                                           reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + bitnet::kStatusOffset),
+                                           reinterpret_cast<cudaStream_t>(stream)),
+                       "rope");
+}
+
+bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld, const int32_t *pos, const int32_t *seq,
+                                 const float *table, int64_t n_pos, int64_t T, int64_t n_heads, int64_t rot_dim,
+                                 int32_t layout, const bitnet_kv_cache *cache, const int32_t *pages, int64_t n_seqs,
+                                 int64_t max_pages, void *Q, void *ws, size_t ws_bytes, bitnet_stream_t stream) {
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16) return fail(BITNET_ERR_INVALID_ARG, "rope_append: bad dtype");
+    bitnet::KvCacheHost c;
+    bitnet_status st = kv_cache_check("rope_append", cache, &c);
+    if (st != BITNET_OK) return st;
+    if (T < 0 || n_heads < 1 || n_seqs < 0 || max_pages < 1) return fail(BITNET_ERR_INVALID_ARG, "rope_append: bad sizes");
+    if (n_heads > 65535 || T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "rope_append: T or n_heads too large");
+    if (ld < (n_heads + 2 * static_cast<int64_t>(c.n_kv_heads)) * c.head_dim)
+        return fail(BITNET_ERR_INVALID_ARG, "rope_append: a row holds (n_heads + 2 n_kv_heads) * head_dim elements");
+    st = rope_table_check("rope_append", table, n_pos, rot_dim, c.head_dim, layout);
+    if (st != BITNET_OK) return st;
+    st = status_ws_check("rope_append", ws, ws_bytes);
+    if (st != BITNET_OK) return st;
+    if (!seq && T > n_seqs) return fail(BITNET_ERR_INVALID_ARG, "rope_append: without seq, row t belongs to sequence t: T <= n_seqs");
+    if (T == 0) return BITNET_OK;   // an empty batch needs no buffers
+    if (!QKV || !Q || !pos || !pages) return fail(BITNET_ERR_INVALID_ARG, "rope_append: null pointer");
+    const size_t es = dtype == BITNET_F32 ? 4 : 2;
+    if (!aligned(QKV, es) || !aligned(Q, 2) || !aligned(pos, 4) || !aligned(seq, 4) || !aligned(pages, 4))
+        return fail(BITNET_ERR_INVALID_ARG, "rope_append: an argument is not aligned to its elements");
+    const size_t row = static_cast<size_t>((n_heads + 2 * static_cast<int64_t>(c.n_kv_heads)) * c.head_dim);
+    const size_t xb = (static_cast<size_t>(T - 1) * static_cast<size_t>(ld) + row) * es;
+    if (overlaps(QKV, xb, Q, static_cast<size_t>(T) * static_cast<size_t>(n_heads * c.head_dim) * 2))
+        return fail(BITNET_ERR_INVALID_ARG, "rope_append: Q overlaps QKV");
+    return cuda_status(bitnet::launch_rope_append(QKV, dtype == BITNET_BF16, ld, pos, seq, table, n_pos, T, n_heads, rot_dim,
+                                                  layout == BITNET_ROPE_INTERLEAVED, c, pages, n_seqs, max_pages, Q,
+                                                  reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + bitnet::kStatusOffset),
+                                                  reinterpret_cast<cudaStream_t>(stream)),
+                       "rope_append");
+}
+
 bitnet_status bitnet_sparse_linear(const int8_t *Xq, const float *absmax, const bitnet_packed_w *W, int64_t T,
                                    void *Y, bitnet_dtype y_dtype, int32_t *acc_out, void *ws, size_t ws_bytes,
                                    bitnet_stream_t stream) {
@@ -618,7 +716,9 @@ bitnet_status bitnet_read_device_status(void *ws, bitnet_stream_t stream) {
                             cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
         if (e != cudaSuccess) return cuda_status(e, "read_device_status");
-        return fail(BITNET_ERR_TIMEOUT, "a device-side bounded wait gave up (status word 0x%x)", word);
+        if (word & 1u) return fail(BITNET_ERR_TIMEOUT, "a device-side bounded wait gave up (status word 0x%x)", word);
+        return fail(BITNET_ERR_INVALID_ARG, "a position, sequence, page or length on the device was out of range "
+                                            "(status word 0x%x)", word);
     }
     return BITNET_OK;
 }

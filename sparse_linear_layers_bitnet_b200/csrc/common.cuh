@@ -10,8 +10,9 @@
 
 namespace bitnet {
 
-// Device status word values (first 4 bytes of every workspace).
+// Device status word bits (first 4 bytes of every workspace).
 constexpr uint32_t kStatusTimeout = 1u;
+constexpr uint32_t kStatusBadIndex = 2u;   // a position, sequence, page or length on the device was out of range
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s

@@ -119,6 +119,20 @@ cudaError_t launch_rmsnorm_grad(const void *dY, bool dy_bf16, const void *H, con
                                 const void *dR, bool g_bf16, int64_t T, int64_t K, void *dH, float *dw, bool accumulate,
                                 void *ws, cudaStream_t s);
 
+// Rotary positions and the paged key-value cache (rope.cu)
+struct KvCacheHost {
+    void *k, *v;
+    int64_t n_pages, page_stride, head_stride, row_stride;   // strides in elements
+    int page_shift, n_kv_heads, head_dim;
+};
+cudaError_t launch_rope(const void *X, bool bf16, int64_t ldx, const int32_t *pos, const float *table, int64_t n_pos,
+                        int64_t T, int64_t heads, int64_t head_dim, int64_t rot_dim, bool interleaved, bool inverse, void *Y,
+                        int64_t ldy, uint32_t *status, cudaStream_t s);
+cudaError_t launch_rope_append(const void *QKV, bool bf16, int64_t ld, const int32_t *pos, const int32_t *seq,
+                               const float *table, int64_t n_pos, int64_t T, int64_t n_heads, int64_t rot_dim,
+                               bool interleaved, const KvCacheHost &c, const int32_t *pages, int64_t n_seqs,
+                               int64_t max_pages, void *Q, uint32_t *status, cudaStream_t s);
+
 cudaError_t launch_gemv_dec(const int8_t *Xq, const float *amax, const float *gamma, const uint8_t *dec,
                             int64_t T, int64_t n_out, int64_t k, void *Y, bool y_bf16, int32_t *acc,
                             cudaStream_t s);

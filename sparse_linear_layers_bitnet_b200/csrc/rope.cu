@@ -1,0 +1,256 @@
+// Rotary positions, and the write of keys and values into a paged cache (sm_100a).
+//
+// A pair (a, b) of a head's features is turned by the angle of its position
+// and frequency, with (c, s) = (cos, sin) read from an fp32 table:
+//   a' = fp32(fp32(a c) - fp32(b s)),   b' = fp32(fp32(b c) + fp32(a s)),
+// each step one rounded fp32 operation, then one rounding to the output's
+// type, so the result is the same bit for bit everywhere.  The inverse (the
+// backward pass: the rotation is orthogonal) takes -s.
+//
+// Memory-bound: every head is read once and written once.  A thread owns one
+// place of the head (two vectors of VEC features that hold VEC pairs) and walks
+// over heads, so it reads its (c, s) once per token and keeps them in registers.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bitnet {
+
+namespace {
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC <= 16 ? sizeof(T) * VEC : 16) Vec {
+    T v[VEC];
+};
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+struct RopeParams {
+    const void *x;            // input rows
+    int64_t ldx;
+    void *y;                  // rotated heads (rope) or the query heads (append)
+    int64_t ldy;
+    const int32_t *pos;
+    const float2 *table;      // [n_pos, rot / 2] (cos, sin); NULL with rot = 0
+    int64_t n_pos;
+    int64_t T;
+    int heads;                // heads per row that are rotated and go to y
+    int kv_heads;             // append: key heads, then value heads behind them
+    int head_dim, rot, inverse;
+    int places;               // threads per head
+    int slots;                // heads a CTA holds at once
+    // append
+    void *k, *v;
+    int64_t page_stride, head_stride, row_stride;
+    const int32_t *pages;     // [n_seqs, max_pages]
+    const int32_t *seq;       // [T] or NULL (row t is sequence t)
+    int64_t n_seqs, max_pages, n_pages;
+    int page_shift;
+    uint32_t *status;
+};
+
+constexpr int kRopeHeads = 4;   // heads a thread has in flight
+
+template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
+__global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t t = blockIdx.x;
+    const int place = threadIdx.x % p.places, slot = threadIdx.x / p.places;
+    if (slot >= p.slots) return;
+    // the row's position, and for the cache its sequence, page and row in the page
+    const int pos = __ldg(p.pos + t);
+    if (pos < 0) return;   // a padding row
+    int64_t cache_row = 0;
+    bool bad = p.rot > 0 && pos >= p.n_pos;
+    if (APPEND) {
+        const int64_t seq = p.seq ? static_cast<int64_t>(__ldg(p.seq + t)) : t;
+        if (seq < 0) return;   // a padding row
+        const int64_t in_table = pos >> p.page_shift;
+        bad = bad || seq >= p.n_seqs || in_table >= p.max_pages;
+        if (!bad) {
+            const int64_t page = __ldg(p.pages + seq * p.max_pages + in_table);
+            bad = page < 0 || page >= p.n_pages;
+            cache_row = page * p.page_stride + static_cast<int64_t>(pos & ((1 << p.page_shift) - 1)) * p.row_stride;
+        }
+    }
+    if (bad) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+        return;
+    }
+    // this place's two vectors: pairs below `turned`, copied features behind them
+    const int half = p.rot >> 1;
+    const int turned = half / VEC;   // places that rotate
+    const bool turns = place < turned;
+    int off_a, off_b;
+    bool has_b = true;
+    if (turns) {
+        off_a = INTERLEAVED ? 2 * VEC * place : VEC * place;
+        off_b = INTERLEAVED ? off_a + VEC : half + off_a;
+    } else {
+        off_a = p.rot + 2 * VEC * (place - turned);
+        off_b = off_a + VEC;
+        has_b = off_b < p.head_dim;
+    }
+    float c[VEC], s[VEC];
+    if (turns) {
+        const float2 *row = p.table + static_cast<int64_t>(pos) * half + VEC * place;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float2 cs = __ldg(row + i);
+            c[i] = cs.x;
+            s[i] = p.inverse ? -cs.y : cs.y;
+        }
+    }
+    const TI *x = static_cast<const TI *>(p.x) + t * p.ldx;
+    TO *y = static_cast<TO *>(p.y) + t * p.ldy;
+    const int all = p.heads + 2 * p.kv_heads;
+    using VI = Vec<TI, VEC>;
+    using VO = Vec<TO, VEC>;
+    for (int h0 = blockIdx.y * p.slots * kRopeHeads + slot; h0 < all; h0 += gridDim.y * p.slots * kRopeHeads) {
+        VI a[kRopeHeads], b[kRopeHeads];
+#pragma unroll
+        for (int j = 0; j < kRopeHeads; ++j) {
+            const int h = h0 + j * p.slots;
+            if (h < all) {
+                const TI *src = x + static_cast<int64_t>(h) * p.head_dim;
+                a[j] = *reinterpret_cast<const VI *>(src + off_a);
+                if (has_b) b[j] = *reinterpret_cast<const VI *>(src + off_b);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRopeHeads; ++j) {
+            const int h = h0 + j * p.slots;
+            if (h >= all) continue;
+            TO *dst = y + static_cast<int64_t>(h) * p.head_dim;
+            if (APPEND && h >= p.heads) {
+                const int kh = h - p.heads;
+                dst = kh < p.kv_heads ? static_cast<TO *>(p.k) + cache_row + kh * p.head_stride
+                                      : static_cast<TO *>(p.v) + cache_row + (kh - p.kv_heads) * p.head_stride;
+            }
+            VO u, w;
+            if (turns && !(APPEND && h >= p.heads + p.kv_heads)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved)
+                    float fa, fb;
+                    if (INTERLEAVED) {
+                        fa = widen(2 * i < VEC ? a[j].v[(2 * i) % VEC] : b[j].v[(2 * i) % VEC]);
+                        fb = widen(2 * i + 1 < VEC ? a[j].v[(2 * i + 1) % VEC] : b[j].v[(2 * i + 1) % VEC]);
+                    } else {
+                        fa = widen(a[j].v[i]);
+                        fb = widen(b[j].v[i]);
+                    }
+                    const TO ra = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
+                    const TO rb = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
+                    if (INTERLEAVED) {
+                        if (2 * i < VEC) u.v[(2 * i) % VEC] = ra; else w.v[(2 * i) % VEC] = ra;
+                        if (2 * i + 1 < VEC) u.v[(2 * i + 1) % VEC] = rb; else w.v[(2 * i + 1) % VEC] = rb;
+                    } else {
+                        u.v[i] = ra;
+                        w.v[i] = rb;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    u.v[i] = narrow<TO>(widen(a[j].v[i]));
+                    w.v[i] = has_b ? narrow<TO>(widen(b[j].v[i])) : u.v[i];
+                }
+            }
+            *reinterpret_cast<VO *>(dst + off_a) = u;
+            if (has_b) *reinterpret_cast<VO *>(dst + off_b) = w;
+        }
+    }
+}
+
+// whether every vector access of VEC features is aligned
+bool fits(const RopeParams &p, int vec, int in_size, int out_size, bool interleaved, bool append) {
+    auto on = [&](const void *q, int size) {
+        const int n = size * vec < 16 ? size * vec : 16;
+        return (reinterpret_cast<uintptr_t>(q) & static_cast<uintptr_t>(n - 1)) == 0;
+    };
+    if (p.head_dim % vec || p.rot % vec || p.ldx % vec || p.ldy % vec) return false;
+    if (interleaved ? p.rot % (2 * vec) : (p.rot / 2) % vec) return false;
+    if (!on(p.x, in_size) || !on(p.y, out_size)) return false;
+    if (append && (p.page_stride % vec || p.head_stride % vec || p.row_stride % vec || !on(p.k, out_size) || !on(p.v, out_size)))
+        return false;
+    return true;
+}
+
+template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
+cudaError_t go(RopeParams p, cudaStream_t s) {
+    const int half = p.rot / 2;
+    const int all = p.heads + 2 * p.kv_heads;
+    p.places = half / VEC + (p.head_dim - p.rot + 2 * VEC - 1) / (2 * VEC);
+    int slots = 256 / p.places;
+    if (slots < 1) slots = 1;
+    if (slots > all) slots = all;
+    p.slots = slots;
+    // one round of heads per CTA: rows with few tokens still spread over the SMs
+    const int rounds = (all + slots * kRopeHeads - 1) / (slots * kRopeHeads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.T), static_cast<unsigned>(rounds));
+    cfg.blockDim = dim3(static_cast<unsigned>((p.places * slots + 31) / 32 * 32));
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rope<TI, TO, VEC, INTERLEAVED, APPEND>, p);
+}
+
+template <typename TI, typename TO, bool INTERLEAVED, bool APPEND>
+cudaError_t by_vec(const RopeParams &p, cudaStream_t s) {
+    const int in = sizeof(TI), out = sizeof(TO);
+    if (fits(p, 8, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 8, INTERLEAVED, APPEND>(p, s);
+    if (fits(p, 4, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 4, INTERLEAVED, APPEND>(p, s);
+    if (fits(p, 2, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 2, INTERLEAVED, APPEND>(p, s);
+    return go<TI, TO, 1, INTERLEAVED, APPEND>(p, s);
+}
+
+template <typename TI, typename TO, bool APPEND>
+cudaError_t by_layout(const RopeParams &p, bool interleaved, cudaStream_t s) {
+    return interleaved ? by_vec<TI, TO, true, APPEND>(p, s) : by_vec<TI, TO, false, APPEND>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void *X, bool bf16, int64_t ldx, const int32_t *pos, const float *table, int64_t n_pos,
+                        int64_t T, int64_t heads, int64_t head_dim, int64_t rot_dim, bool interleaved, bool inverse, void *Y,
+                        int64_t ldy, uint32_t *status, cudaStream_t s) {
+    RopeParams p = {};
+    p.x = X; p.ldx = ldx; p.y = Y; p.ldy = ldy;
+    p.pos = pos; p.table = reinterpret_cast<const float2 *>(table); p.n_pos = n_pos;
+    p.T = T; p.heads = static_cast<int>(heads); p.kv_heads = 0;
+    p.head_dim = static_cast<int>(head_dim); p.rot = static_cast<int>(rot_dim); p.inverse = inverse ? 1 : 0;
+    p.status = status;
+    return bf16 ? by_layout<__nv_bfloat16, __nv_bfloat16, false>(p, interleaved, s)
+                : by_layout<float, float, false>(p, interleaved, s);
+}
+
+cudaError_t launch_rope_append(const void *QKV, bool bf16, int64_t ld, const int32_t *pos, const int32_t *seq,
+                               const float *table, int64_t n_pos, int64_t T, int64_t n_heads, int64_t rot_dim,
+                               bool interleaved, const KvCacheHost &c, const int32_t *pages, int64_t n_seqs,
+                               int64_t max_pages, void *Q, uint32_t *status, cudaStream_t s) {
+    RopeParams p = {};
+    p.x = QKV; p.ldx = ld; p.y = Q; p.ldy = n_heads * c.head_dim;
+    p.pos = pos; p.table = reinterpret_cast<const float2 *>(table); p.n_pos = n_pos;
+    p.T = T; p.heads = static_cast<int>(n_heads); p.kv_heads = c.n_kv_heads;
+    p.head_dim = c.head_dim; p.rot = static_cast<int>(rot_dim);
+    p.k = c.k; p.v = c.v;
+    p.page_stride = c.page_stride; p.head_stride = c.head_stride; p.row_stride = c.row_stride;
+    p.pages = pages; p.seq = seq; p.n_seqs = n_seqs; p.max_pages = max_pages; p.n_pages = c.n_pages;
+    p.page_shift = c.page_shift; p.status = status;
+    return bf16 ? by_layout<__nv_bfloat16, __nv_bfloat16, true>(p, interleaved, s)
+                : by_layout<float, __nv_bfloat16, true>(p, interleaved, s);
+}
+
+}  // namespace bitnet

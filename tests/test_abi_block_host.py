@@ -72,3 +72,55 @@ def test_rmsnorm_grad_refusals(lib):
     assert b"overlap" in lib.bitnet_last_error()
     assert call(f, ok, T=0, dw=None) == _abi.BITNET_OK
     assert lib.bitnet_rmsnorm_grad_workspace_size(1, 512) >= 512 * 4
+
+
+def test_rope_refusals(lib):
+    f = lib.bitnet_rope
+    ok = dict(X=at(1), dtype=1, ldx=512, pos=at(2), table=at(3), n_pos=64, T=4, n_heads=4, head_dim=128, rot_dim=128,
+              layout=0, inverse=0, Y=at(4), ldy=512, ws=at(5), ws_bytes=256, stream=None)
+    for name in ("X", "Y", "pos", "table"):
+        assert call(f, ok, **{name: None}) == INVALID, name
+    for name, off in (("X", 1), ("Y", 1), ("pos", 2), ("table", 4), ("ws", 8)):
+        assert call(f, ok, **{name: ok[name] + off}) == INVALID, name
+    for name, bad in (("dtype", 3), ("ldx", 511), ("ldy", 511), ("n_pos", 0), ("T", -1), ("n_heads", 0), ("head_dim", 0),
+                      ("rot_dim", 130), ("rot_dim", 63), ("rot_dim", -2), ("layout", 2)):
+        assert call(f, ok, **{name: bad}) == INVALID, name
+    assert call(f, ok, head_dim=257, ldx=4096, ldy=4096) == UNSUPPORTED
+    assert call(f, ok, T=1 << 31) == UNSUPPORTED
+    assert call(f, ok, ws=None) == WORKSPACE and call(f, ok, ws_bytes=255) == WORKSPACE
+    assert call(f, ok, Y=at(1), ldy=1024) == INVALID and call(f, ok, Y=at(1, 256)) == INVALID
+    assert call(f, ok, T=0, X=None, Y=None, pos=None) == _abi.BITNET_OK
+
+
+def cache(**changed):
+    c = _abi.BitnetKvCache(at(10), at(11), 32, 16 * 5 * 128, 16 * 128, 128, 16, 5, 128)
+    for k, v in changed.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+BAD_CACHES = [("k", None, INVALID), ("v", None, INVALID), ("k", at(10, 8), INVALID), ("n_pages", 0, INVALID),
+              ("n_pages", 1 << 31, UNSUPPORTED), ("page_size", 24, UNSUPPORTED), ("page_size", 4, UNSUPPORTED),
+              ("page_size", 1 << 17, UNSUPPORTED), ("page_size", 0, INVALID), ("n_kv_heads", 0, INVALID),
+              ("n_kv_heads", 65536, UNSUPPORTED), ("head_dim", 257, UNSUPPORTED), ("head_dim", 0, INVALID),
+              ("row_stride", 124, INVALID), ("row_stride", 120, INVALID), ("head_stride", 2044, INVALID),
+              ("page_stride", 8, INVALID)]
+
+
+def test_rope_append_refusals(lib):
+    f = lib.bitnet_rope_append
+    ok = dict(QKV=at(1), dtype=1, ld=3840, pos=at(2), seq=at(3), table=at(4), n_pos=64, T=4, n_heads=20, rot_dim=128,
+              layout=1, cache=cache(), pages=at(5), n_seqs=2, max_pages=8, Q=at(6), ws=at(7), ws_bytes=256, stream=None)
+    for name in ("QKV", "pos", "table", "pages", "Q", "cache"):
+        assert call(f, ok, **{name: None}) == INVALID, name
+    for field, value, status in BAD_CACHES:
+        assert call(f, ok, cache=cache(**{field: value})) == status, field
+    for name, bad in (("dtype", 3), ("ld", 3839), ("n_pos", 0), ("T", -1), ("n_heads", 0), ("n_seqs", -1), ("max_pages", 0),
+                      ("rot_dim", 130), ("rot_dim", 63), ("layout", 2)):
+        assert call(f, ok, **{name: bad}) == INVALID, name
+    assert call(f, ok, seq=None) == INVALID                     # four rows, two sequences
+    assert call(f, ok, Q=at(1, 4096)) == INVALID
+    assert call(f, ok, T=1 << 31) == UNSUPPORTED
+    assert call(f, ok, ws=None) == WORKSPACE and call(f, ok, ws_bytes=0) == WORKSPACE
+    assert call(f, ok, T=0, QKV=None, pos=None, Q=None) == _abi.BITNET_OK
+    assert call(f, ok, T=0, rot_dim=0, table=None, n_pos=0) == _abi.BITNET_OK
