@@ -484,6 +484,42 @@ bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld
                                  int64_t max_pages, void *Q, void *ws, size_t ws_bytes, bitnet_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * bitnet_paged_attn - attention of one new token per sequence over the cache.
+ *
+ * The decode step's attention, between the QKV product and the O product of a
+ * LLaMA-alike block ("BitNet b1.58 ...", section "What this paper explains").
+ * Query head h reads key-value head h / (n_heads / n_kv_heads).  Over the
+ * lens[b] first keys of sequence b, in the order of its page list:
+ *   O[b,h] = sum_j softmax_j(scale q[b,h] . k_j) v_j;
+ *   lse[b,h] = log sum_j exp(scale q[b,h] . k_j)   (natural logarithm).
+ * A sequence without keys (an idle slot of the batch) gets zeros and minus
+ * infinity.  Rows of the cache behind a sequence's length are not used,
+ * whatever they hold.  Scores, their maxima and sums and the output are held in
+ * fp32, a softmax weight in 16 bits of significand; the result repeats bit for
+ * bit.
+ *
+ *   Q         [n_seqs, ldq] bf16, n_heads * head_dim elements of a row are used.
+ *   cache     host struct, read during the call only; n_heads % n_kv_heads == 0.
+ *   pages     [n_seqs, max_pages] int32 (device); max_pages * page_size <= 2^30.
+ *   lens      [n_seqs] int32 (device): keys of each sequence, the new one's
+ *             included.  One that is negative or above max_pages * page_size
+ *             counts as 0 or max_pages * page_size and sets the status word; so
+ *             does a page outside [0, n_pages), whose keys are left out.
+ *   scale     finite, usually head_dim^-1/2.
+ *   O         [n_seqs, ldo] of o_dtype; must not overlap Q.   lse  [n_seqs,
+ *             n_heads] fp32 or NULL.
+ *   ws        >= bitnet_paged_attn_workspace_size(...) bytes, 16-byte aligned:
+ *             status word and partial results (contents ignored).  Calls that
+ *             may run at the same time need workspaces of their own.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------ */
+size_t bitnet_paged_attn_workspace_size(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
+bitnet_status bitnet_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const bitnet_kv_cache *cache,
+                                const int32_t *pages, int64_t max_pages, const int32_t *lens, float scale, void *O,
+                                bitnet_dtype o_dtype, int64_t ldo, float *lse, void *ws, size_t ws_bytes,
+                                bitnet_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * bitnet_swiglu_quant - SwiGLU gate fused into the per-token quantisation.
  *
  * Same pages and sections as bitnet_rmsnorm_quant.  Per token t and column f:

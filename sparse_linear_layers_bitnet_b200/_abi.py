@@ -31,7 +31,8 @@ EXPORTED = [
     "bitnet_pack_6of8_windows", "bitnet_quant_act_lift_6of8",
     "bitnet_quant_act", "bitnet_rmsnorm_quant", "bitnet_add_rmsnorm_quant",
     "bitnet_rmsnorm_grad_workspace_size", "bitnet_rmsnorm_grad",
-    "bitnet_rope_workspace_size", "bitnet_rope", "bitnet_rope_append", "bitnet_swiglu_quant",
+    "bitnet_rope_workspace_size", "bitnet_rope", "bitnet_rope_append",
+    "bitnet_paged_attn_workspace_size", "bitnet_paged_attn", "bitnet_swiglu_quant",
     "bitnet_linear_workspace_size", "bitnet_sparse_linear",
     "bitnet_quant_linear_workspace_size", "bitnet_quant_linear",
     "bitnet_decode_chain_workspace_size", "bitnet_decode_chain",
@@ -142,6 +143,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "bitnet_rope": (I32, [P, I32, I64, P, P, I64, I64, I64, I64, I64, I32, I32, P, I64, P, SZ, P]),
         "bitnet_rope_append": (I32, [P, I32, I64, P, P, P, I64, I64, I64, I64, I32, ctypes.POINTER(BitnetKvCache), P, I64,
                                      I64, P, P, SZ, P]),
+        "bitnet_paged_attn_workspace_size": (SZ, [I64, I64, I64, I64]),
+        "bitnet_paged_attn": (I32, [P, I64, I64, I64, ctypes.POINTER(BitnetKvCache), P, I64, P, F, P, I32, I64, P, P, SZ, P]),
         "bitnet_swiglu_quant": (I32, [P, P, I64, I64, I64, F, P, P, P]),
         "bitnet_linear_workspace_size": (SZ, []),
         "bitnet_sparse_linear": (I32, [P, P, ctypes.POINTER(BitnetPackedW), I64, P, I32, P, P, SZ, P]),
@@ -642,6 +645,31 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
             _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0, ctypes.byref(c), pages.data_ptr(), n_seqs,
             max_pages, Q.data_ptr(), ws_ptr, ws_bytes)
     return Q
+
+
+def bitnet_paged_attn(Q, K, V, pages, lens, scale: float | None = None, O=None, o_dtype=None, lse=None,
+                      ws: "Workspace | None" = None, stream=None):
+    """Attention of one token per sequence: Q bf16 [sequences, heads * head_dim] (rows may be strided) over the
+    first lens (int32 [sequences]) keys of each sequence in the cache K, V by its page list in pages (see
+    bitnet_rope_append).  scale: head_dim^-1/2 unless given.  lse: fp32 [sequences, heads], filled when given.
+    Returns O (bf16 unless o_dtype says fp32)."""
+    torch = _torch()
+    lib = load()
+    c = _cache_struct(K, V)
+    assert Q.dim() == 2 and Q.dtype == torch.bfloat16 and Q.stride(1) == 1 and Q.device == K.device
+    n_seqs, width = Q.shape
+    heads = width // c.head_dim
+    assert heads > 0 and width == heads * c.head_dim
+    assert pages.dim() == 2 and _is(pages, torch.int32, (n_seqs, pages.shape[1]), Q) and _is(lens, torch.int32, (n_seqs,), Q)
+    if O is None:
+        O = _new((n_seqs, width), torch.bfloat16 if o_dtype is None else o_dtype, Q, stream)
+    assert O.shape == Q.shape and O.stride(1) == 1 and O.device == Q.device and (o_dtype is None or O.dtype == o_dtype)
+    assert _is(lse, torch.float32, (n_seqs, heads), Q, optional=True)
+    keep, ws_ptr, ws_bytes = _ws(ws, lib.bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream)
+    _launch("bitnet_paged_attn", Q, stream, Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(),
+            pages.shape[1], lens.data_ptr(), c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(),
+            _dtype_code(O.dtype), _ld(O), _addr(lse), ws_ptr, ws_bytes)
+    return O
 
 
 def bitnet_swiglu_quant(GU, F: int | None = None, eps_act: float = 1e-5, Xq=None, absmax=None, stream=None):

@@ -504,6 +504,42 @@ bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld
                        "rope_append");
 }
 
+size_t bitnet_paged_attn_workspace_size(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
+    return bitnet::paged_attn_ws_bytes(n_seqs, n_heads, n_kv_heads, head_dim);
+}
+
+bitnet_status bitnet_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const bitnet_kv_cache *cache,
+                                const int32_t *pages, int64_t max_pages, const int32_t *lens, float scale, void *O,
+                                bitnet_dtype o_dtype, int64_t ldo, float *lse, void *ws, size_t ws_bytes,
+                                bitnet_stream_t stream) {
+    if (o_dtype != BITNET_F32 && o_dtype != BITNET_BF16) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: bad output dtype");
+    bitnet::KvCacheHost c;
+    const bitnet_status st = kv_cache_check("paged_attn", cache, &c);
+    if (st != BITNET_OK) return st;
+    if (n_seqs < 0 || n_heads < 1 || max_pages < 1) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: bad sizes");
+    if (n_heads % c.n_kv_heads) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: n_heads must be a multiple of n_kv_heads");
+    if (n_heads > 65535 || n_seqs > (1 << 20) || n_seqs * n_heads > 2147483647LL)
+        return fail(BITNET_ERR_UNSUPPORTED, "paged_attn: too many sequences or heads");
+    if (max_pages > (1LL << 30) >> c.page_shift) return fail(BITNET_ERR_UNSUPPORTED, "paged_attn: a page list of more than 2^30 keys");
+    if (!std::isfinite(scale)) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: scale must be finite");
+    const int64_t row = n_heads * c.head_dim;
+    if (ldq < row || ldo < row) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: a row holds n_heads * head_dim elements");
+    if (!ws) return fail(BITNET_ERR_WORKSPACE, "paged_attn: workspace is required");
+    const size_t need = bitnet_paged_attn_workspace_size(n_seqs, n_heads, c.n_kv_heads, c.head_dim);
+    if (ws_bytes < need) return fail(BITNET_ERR_WORKSPACE, "paged_attn: workspace needs %zu bytes", need);
+    if (!aligned(ws, 16)) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: ws must be 16-byte aligned");
+    if (n_seqs == 0) return BITNET_OK;   // an empty batch needs no buffers
+    if (!Q || !O || !pages || !lens) return fail(BITNET_ERR_INVALID_ARG, "paged_attn: null pointer");
+    const size_t es = o_dtype == BITNET_F32 ? 4 : 2;
+    if (!aligned(Q, 2) || !aligned(O, es) || !aligned(pages, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+        return fail(BITNET_ERR_INVALID_ARG, "paged_attn: an argument is not aligned to its elements");
+    if (overlaps(Q, static_cast<size_t>((n_seqs - 1) * ldq + row) * 2, O, static_cast<size_t>((n_seqs - 1) * ldo + row) * es))
+        return fail(BITNET_ERR_INVALID_ARG, "paged_attn: O overlaps Q");
+    return cuda_status(bitnet::launch_paged_attn(Q, ldq, n_seqs, n_heads, c, pages, max_pages, lens, scale, O,
+                                                 o_dtype == BITNET_BF16, ldo, lse, ws, reinterpret_cast<cudaStream_t>(stream)),
+                       "paged_attn");
+}
+
 bitnet_status bitnet_sparse_linear(const int8_t *Xq, const float *absmax, const bitnet_packed_w *W, int64_t T,
                                    void *Y, bitnet_dtype y_dtype, int32_t *acc_out, void *ws, size_t ws_bytes,
                                    bitnet_stream_t stream) {

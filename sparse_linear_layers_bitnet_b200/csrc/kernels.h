@@ -133,6 +133,13 @@ cudaError_t launch_rope_append(const void *QKV, bool bf16, int64_t ld, const int
                                bool interleaved, const KvCacheHost &c, const int32_t *pages, int64_t n_seqs,
                                int64_t max_pages, void *Q, uint32_t *status, cudaStream_t s);
 
+// One-token attention over the paged cache (paged_attn.cu)
+constexpr int kAttnMaxCtas = 4;   // CTAs per SM at most (sizes the partials)
+size_t paged_attn_ws_bytes(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
+cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const KvCacheHost &c,
+                              const int32_t *pages, int64_t max_pages, const int32_t *lens, float scale, void *O, bool o_bf16,
+                              int64_t ldo, float *lse, void *ws, cudaStream_t s);
+
 cudaError_t launch_gemv_dec(const int8_t *Xq, const float *amax, const float *gamma, const uint8_t *dec,
                             int64_t T, int64_t n_out, int64_t k, void *Y, bool y_bf16, int32_t *acc,
                             cudaStream_t s);

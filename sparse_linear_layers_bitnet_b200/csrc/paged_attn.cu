@@ -1,0 +1,636 @@
+// Attention of one new token per sequence over a paged bf16 key-value cache (sm_100a).
+//
+// Per sequence and query head: o = sum_j p_j v_j / sum_j p_j with
+// p_j = 2^(x_j - m), x_j = (q . k_j) scale log2 e and m the largest x_j, in one
+// pass over the keys with a running m, sum and o (rescaled when m grows).
+//
+// Bound: HBM.  Every key and value is read once and used for the few query
+// heads that share it, a handful of operations per byte.  So:
+//  * The work of a call, in units of 64 keys of one key-value head, is cut into
+//    one equal contiguous range per CTA (whatever the lengths are), and a CTA
+//    writes an unnormalised partial (m, sum, o) for a head whose keys it holds
+//    only a part of; a second small launch joins those.  The cut depends only
+//    on the lengths, so results repeat bit for bit.
+//  * Each of a CTA's four warps takes 16 keys of a unit.  A lane copies the
+//    16-byte pieces that it will itself use into its own shared-memory slots
+//    (cp.async, several pieces of 4 KB per warp in flight) and reads them back
+//    from there: no barrier, no bank conflict, no fragment shuffle.
+//  * Products on mma.sync m16n8k16 with 16 keys (or 16 features of the values)
+//    as rows and 8 query heads as columns: S^T = K Q^T, then O^T += V^T P^T.
+//    The contraction index may be permuted at will, so K's fragments are the 16
+//    bytes a lane loaded, and V^T's are byte permutes of two rows' words.  S^T
+//    becomes the P^T operand by an 8 x 8 transpose per warp (movmatrix).  p is
+//    split into a bf16 high and low part (two MMAs), which keeps 16 bits of it:
+//    with a single bf16 p its rounding alone would be as large as that of the
+//    bf16 output.  The tensor pipe is far from being the bound.
+#include "common.cuh"
+#include "kernels.h"
+
+#include <atomic>
+
+namespace bitnet {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kUnit = 16 * kWarps;   // keys per unit
+
+struct AttnParams {
+    const __nv_bfloat16 *q;
+    int64_t ldq;
+    const __nv_bfloat16 *k, *v;
+    int64_t page_stride, head_stride, row_stride;
+    const int32_t *pages;
+    int64_t max_pages, n_pages;
+    int page_shift;
+    const int32_t *lens;
+    int n_seqs, n_heads, group;       // group: query heads per key-value head
+    int vheads, vper, per_vhead;      // virtual key-value heads: vheads = kv heads x vper, each with up to per_vhead query heads
+    int head_dim;
+    float scale_log2;                 // scale log2 e
+    void *o;
+    int64_t ldo;
+    int o_bf16;
+    float *lse;                       // or NULL
+    float *part;                      // [grid, 2] partials
+    uint32_t *status;
+    int grid;                         // CTAs of the first launch (those behind the number of units stay idle)
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// high and low bf16 parts of a pair, packed
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// a sequence's length, held to what its page list can hold
+__device__ __forceinline__ int length_of(const AttnParams &p, int b) {
+    int64_t n = __ldg(p.lens + b);
+    const int64_t cap = p.max_pages << p.page_shift;
+    return static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
+}
+__device__ __forceinline__ int64_t units_of(const AttnParams &p, int b) {
+    return static_cast<int64_t>((length_of(p, b) + kUnit - 1) / kUnit) * p.vheads;
+}
+
+// Sum of units over the sequences below `upto` (exclusive), by the whole CTA of 128 threads.
+__device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *s_warp) {
+    int64_t s = 0;
+    for (int b = threadIdx.x; b < upto; b += blockDim.x) s += units_of(p, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0;
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += s_warp[i];
+    return s;
+}
+
+// The sequence that holds unit u, and the units before it: the CTA scans blockDim.x sequences at a time.
+__device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t *s_scan, int *s_at) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        const int64_t mine = b < p.n_seqs ? units_of(p, b) : 0;
+        int64_t s = mine;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += x;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) *s_at = -1;
+        if (lane == 31) s_scan[warp] = s;
+        __syncthreads();
+        int64_t all = 0, base = before;
+        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) {
+            if (i < warp) base += s_scan[i];
+            all += s_scan[i];
+        }
+        const int64_t end = base + s, start = end - mine;
+        if (start <= u && u < end) {
+            *s_at = b;
+            s_scan[kWarps] = start;
+        }
+        __syncthreads();
+        if (*s_at >= 0) {
+            *first = s_scan[kWarps];
+            return *s_at;
+        }
+        before += all;
+    }
+    return p.n_seqs;   // not reached for u below the total
+}
+
+// first unit of CTA i's range
+__device__ __forceinline__ int64_t range_start(int64_t units, int ctas, int i) { return units * i / ctas; }
+
+// floats of one partial: per query head head_dim of o, then m and the sum
+__host__ __device__ __forceinline__ int64_t part_floats(int per_vhead, int head_dim) {
+    return static_cast<int64_t>(per_vhead) * (head_dim + 2);
+}
+
+// DB: 64-feature blocks (head_dim <= 64 DB), NT: tiles of 8 query heads, ST: pieces a warp has in its ring
+template <int DB, int NT, int ST>
+__global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) {
+    constexpr int D = 64 * DB;
+    constexpr int kPieces = D / 16;               // 16-byte pieces per lane of one tile (16 keys x D features)
+    constexpr uint32_t kTile = kPieces * 512;     // bytes of one tile
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps + 1];
+    __shared__ int s_at;
+    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // sequences without keys: zeros, and a log-sum of minus infinity
+    for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
+        const int n = __ldg(p.lens + b);
+        if (threadIdx.x == 0 && (n < 0 || n > (p.max_pages << p.page_shift))) atomicOr(p.status, kStatusBadIndex);
+        if (n > 0) continue;
+        for (int i = threadIdx.x; i < p.n_heads * p.head_dim; i += blockDim.x) {
+            if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + i] = __float2bfloat16_rn(0.0f);
+            else static_cast<float *>(p.o)[b * p.ldo + i] = 0.0f;
+        }
+        if (p.lse)
+            for (int i = threadIdx.x; i < p.n_heads; i += blockDim.x)
+                p.lse[static_cast<int64_t>(b) * p.n_heads + i] = -INFINITY;
+    }
+
+    const int64_t units = sum_units(p, p.n_seqs, s_scan);
+    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);   // every one of them gets a unit
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    const int64_t lo = range_start(units, ctas, blockIdx.x), hi = range_start(units, ctas, blockIdx.x + 1);
+    int64_t first = 0;
+    int b = find_seq(p, lo, &first, s_scan, &s_at);
+
+    const uint32_t ring = smem_u32(smem) + warp * (ST * kTile) + lane * 16;
+    // words of the last 16-byte piece of a row that hold features (head_dim not a multiple of 8)
+    const int last_piece = (p.head_dim - 1) >> 3, tail = p.head_dim - 8 * last_piece;
+
+    int64_t u = lo;
+    while (u < hi) {
+        const int len = length_of(p, b);
+        const int64_t n_units = (len + kUnit - 1) / kUnit;
+        if (u >= first + n_units * p.vheads) {   // behind this sequence
+            first += n_units * p.vheads;
+            ++b;
+            continue;
+        }
+        const int vh = static_cast<int>((u - first) / n_units);
+        const int64_t seg_first = first + vh * n_units, seg_end = seg_first + n_units;
+        const int64_t end = seg_end < hi ? seg_end : hi;
+        const int kvh = vh / p.vper, head0 = kvh * p.group + (vh % p.vper) * p.per_vhead;
+        const int heads = min(p.per_vhead, (kvh + 1) * p.group - head0);
+
+        // Q fragments: column g of tile n is query head head0 + 8 n + g; piece i of lane (g, t) is
+        // features 32 i + 8 t .. + 7, the same that the lane holds of a key
+        uint4 qf[NT][D / 32];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int h = 8 * n + g, f = 32 * i + 8 * t;
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (h < heads) {
+                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + b * p.ldq +
+                                          static_cast<int64_t>(head0 + h) * p.head_dim;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (f + e < p.head_dim) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + f + e)) << (16 * (e & 1));
+                }
+                qf[n][i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+
+        float o[NT][DB][4][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][d][w][c] = 0.0f;
+        }
+
+        // this warp's tiles: 16 keys from key0, + 64, ...
+        const int key0 = static_cast<int>((u - seg_first) * kUnit) + 16 * warp;
+        const int key_end = min(len, static_cast<int>((end - seg_first) * kUnit));
+        const int tiles = key_end > key0 ? (key_end - key0 + kUnit - 1) / kUnit : 0;
+        const __nv_bfloat16 *kbase = p.k + kvh * p.head_stride, *vbase = p.v + kvh * p.head_stride;
+        const int32_t *list = p.pages + b * p.max_pages;
+
+        // pages of the 8-key halves of the next tile to be copied (a page holds at least 8 keys)
+        auto page_of = [&](int key) { return key < key_end ? __ldg(list + (key >> p.page_shift)) : -1; };
+        int issue_key = key0, issued = 0;
+        int next0 = page_of(key0), next1 = page_of(key0 + 8);
+        int cur0 = 0, cur1 = 0;
+        uint32_t ok_bits = 0;   // two bits per tile in flight: its halves' pages are valid
+        int slot = 0;           // ring slot of the next piece to be copied
+        auto issue = [&]() {    // copies the next tile of the sequence K0 V0 K1 V1 ...
+            if (issued < 2 * tiles) {
+                const uint32_t dst = ring + slot * kTile;
+                const int row_mask = (1 << p.page_shift) - 1;
+                if ((issued & 1) == 0) {
+                    cur0 = next0;
+                    cur1 = next1;
+                    const bool ok0 = cur0 >= 0 && cur0 < p.n_pages, ok1 = cur1 >= 0 && cur1 < p.n_pages;
+                    const int sh = 2 * ((issued >> 1) & 7);
+                    ok_bits = (ok_bits & ~(3u << sh)) | ((ok0 ? 1u : 0u) << sh) | ((ok1 ? 2u : 0u) << sh);
+                    if (lane == 0 && ((!ok0 && issue_key < key_end) || (!ok1 && issue_key + 8 < key_end)))
+                        atomicOr(p.status, kStatusBadIndex);
+                    next0 = page_of(issue_key + kUnit);
+                    next1 = page_of(issue_key + kUnit + 8);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int key = issue_key + 8 * r + g;
+                        const bool in = key < key_end && (r ? ok1 : ok0);
+                        const __nv_bfloat16 *src = kbase + (in ? (r ? cur1 : cur0) * p.page_stride + (key & row_mask) * p.row_stride : 0);
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const int piece = 4 * i + t;
+                            const bool have = in && piece <= last_piece;
+                            cp16(dst + (r * (D / 32) + i) * 512, src + (have ? 8 * piece : 0), have);
+                        }
+                    }
+                } else {
+                    const int sh = 2 * ((issued >> 1) & 7);
+                    const bool ok0 = (ok_bits >> sh) & 1u, ok1 = (ok_bits >> sh) & 2u;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int key = issue_key + 8 * (r >> 1) + 2 * t + (r & 1);
+                        const bool in = key < key_end && ((r >> 1) ? ok1 : ok0);
+                        const __nv_bfloat16 *src = vbase + (in ? ((r >> 1) ? cur1 : cur0) * p.page_stride + (key & row_mask) * p.row_stride : 0);
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            const int piece = 8 * d + g;
+                            const bool have = in && piece <= last_piece;
+                            cp16(dst + (r * DB + d) * 512, src + (have ? 8 * piece : 0), have);
+                        }
+                    }
+                    issue_key += kUnit;
+                }
+                ++issued;
+                slot = slot + 1 == ST ? 0 : slot + 1;
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) issue();
+
+        int use = 0;   // ring slot of the next piece to be used
+        for (int tile = 0; tile < tiles; ++tile) {
+            // S^T = K Q^T: rows are keys g and g + 8, columns the heads 2 t and 2 t + 1 of each tile
+            cp_wait<ST - 2>();
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            {
+                const uint32_t src = ring + use * kTile;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint4 a = lds16(src + i * 512), c = lds16(src + (D / 32 + i) * 512);
+                    if (tail < 8 && 4 * i + t == last_piece) {   // what lies behind head_dim may be anything
+                        uint32_t *aw = reinterpret_cast<uint32_t *>(&a), *cw = reinterpret_cast<uint32_t *>(&c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t keep = tail >= 2 * e + 2 ? 0xffffffffu : tail == 2 * e + 1 ? 0xffffu : 0u;
+                            aw[e] &= keep;
+                            cw[e] &= keep;
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma(s[n], a.x, c.x, a.y, c.y, qf[n][i].x, qf[n][i].y);
+                        mma(s[n], a.z, c.z, a.w, c.w, qf[n][i].z, qf[n][i].w);
+                    }
+                }
+            }
+            use = use + 1 == ST ? 0 : use + 1;
+            issue();
+
+            // mask, running maximum, p
+            const int key = key0 + tile * kUnit + g;
+            const uint32_t okb = ok_bits >> (2 * (tile & 7));
+            const bool in0 = key < key_end && (okb & 1u), in1 = key + 8 < key_end && (okb & 2u);
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[n][c] = (c < 2 ? in0 : in1) ? s[n][c] * p.scale_log2 : -INFINITY;
+                float x0 = fmaxf(s[n][0], s[n][2]), x1 = fmaxf(s[n][1], s[n][3]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
+                }
+                const float m0 = fmaxf(m[n][0], x0), m1 = fmaxf(m[n][1], x1);
+                if (__any_sync(0xffffffffu, m0 > m[n][0] || m1 > m[n][1])) {
+                    // factors 2^(old - new); an old maximum of minus infinity gives 0
+                    const float f0 = m0 == m[n][0] ? 1.0f : exp2_fast(m[n][0] - m0);
+                    const float f1 = m1 == m[n][1] ? 1.0f : exp2_fast(m[n][1] - m1);
+                    l[n][0] *= f0;
+                    l[n][1] *= f1;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            o[n][d][w][0] *= f0;
+                            o[n][d][w][1] *= f1;
+                            o[n][d][w][2] *= f0;
+                            o[n][d][w][3] *= f1;
+                        }
+                    m[n][0] = m0;
+                    m[n][1] = m1;
+                }
+                const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+                const float p0 = exp2_fast(s[n][0] - z0), p1 = exp2_fast(s[n][1] - z1);
+                const float p2 = exp2_fast(s[n][2] - z0), p3 = exp2_fast(s[n][3] - z1);
+                l[n][0] += p0 + p2;
+                l[n][1] += p1 + p3;
+                split2(p0, p1, ph[n][0], pl[n][0]);
+                split2(p2, p3, ph[n][1], pl[n][1]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    ph[n][r] = transpose8x8(ph[n][r]);
+                    pl[n][r] = transpose8x8(pl[n][r]);
+                }
+            }
+
+            // O^T += V^T P^T: lane (g, t) holds features 64 d + 8 g .. + 7 of keys 2t, 2t+1, 2t+8, 2t+9
+            cp_wait<ST - 2>();
+            {
+                const uint32_t src = ring + use * kTile;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const uint4 v0 = lds16(src + d * 512), v1 = lds16(src + (DB + d) * 512);
+                    const uint4 v2 = lds16(src + (2 * DB + d) * 512), v3 = lds16(src + (3 * DB + d) * 512);
+                    const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                    const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
+                        const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
+                        const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma(o[n][d][w], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                            mma(o[n][d][w], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                        }
+                    }
+                }
+            }
+            use = use + 1 == ST ? 0 : use + 1;
+            issue();
+        }
+        cp_wait<0>();
+
+        // join the four warps through shared memory (the ring is empty now)
+        float *s_o = reinterpret_cast<float *>(smem);   // [warp][head][D]
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+                l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], w);
+                l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], w);
+            }
+            if (g == 0) {
+                s_m[warp][8 * n + 2 * t] = m[n][0];
+                s_m[warp][8 * n + 2 * t + 1] = m[n][1];
+                s_l[warp][8 * n + 2 * t] = l[n][0];
+                s_l[warp][8 * n + 2 * t + 1] = l[n][1];
+            }
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float4 *dst = reinterpret_cast<float4 *>(s_o + (warp * 8 * NT + 8 * n + 2 * t + c) * D + 64 * d + 8 * g);
+                    dst[0] = make_float4(o[n][d][0][c], o[n][d][0][2 + c], o[n][d][1][c], o[n][d][1][2 + c]);
+                    dst[1] = make_float4(o[n][d][2][c], o[n][d][2][2 + c], o[n][d][3][c], o[n][d][3][2 + c]);
+                }
+        }
+        __syncthreads();
+        const bool whole = u == seg_first && end == seg_end;
+        float *part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (u == lo ? 0 : 1)) * part_floats(p.per_vhead, p.head_dim);
+        for (int h = warp; h < heads; h += kWarps) {
+            float top = s_m[0][h];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][h]);
+            const float z = top == -INFINITY ? 0.0f : top;
+            float f[kWarps], sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                f[i] = exp2_fast(s_m[i][h] - z);
+                sum += f[i] * s_l[i][h];
+            }
+            const float inv = whole ? (sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum)) : 1.0f;
+            const int64_t head = head0 + h;
+            for (int d = lane; d < p.head_dim; d += 32) {
+                float x = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) x += f[i] * s_o[(i * 8 * NT + h) * D + d];
+                x *= inv;
+                if (!whole) part[h * p.head_dim + d] = x;
+                else if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(x);
+                else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = x;
+            }
+            if (lane == 0) {
+                if (!whole) {
+                    part[p.per_vhead * p.head_dim + 2 * h] = top;
+                    part[p.per_vhead * p.head_dim + 2 * h + 1] = sum;
+                } else if (p.lse) {
+                    p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
+                }
+            }
+        }
+        __syncthreads();   // the ring is free again
+        u = end;
+    }
+}
+
+// Joins the partials of the heads that more than one CTA of the first launch worked on: CTA (b, virtual head).
+__global__ void __launch_bounds__(128) k_paged_attn_join(const AttnParams p) {
+    __shared__ int64_t s_warp[kWarps + 1];
+    __shared__ float s_top[kWarps], s_sum[kWarps];
+    __shared__ float s_o[kWarps][256];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.x / p.vheads, vh = blockIdx.x % p.vheads;
+    const int len = length_of(p, b);
+    const int64_t n_units = (len + kUnit - 1) / kUnit;
+    if (n_units < 2) return;
+    const int64_t units = sum_units(p, p.n_seqs, s_warp);
+    const int64_t first = sum_units(p, b, s_warp) + vh * n_units, end = first + n_units;
+    // CTA of unit u: the largest i with range_start(i) <= u
+    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);
+    const int i0 = static_cast<int>(((first + 1) * ctas - 1) / units), i1 = static_cast<int>((end * ctas - 1) / units);
+    if (i0 == i1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kvh = vh / p.vper, head0 = kvh * p.group + (vh % p.vper) * p.per_vhead;
+    const int heads = min(p.per_vhead, (kvh + 1) * p.group - head0);
+    const int64_t size = part_floats(p.per_vhead, p.head_dim);
+    for (int h = 0; h < heads; ++h) {
+        // each warp joins every fourth partial, then the four are joined
+        float top = -INFINITY, sum = 0.0f, o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+        for (int i = i0 + warp; i <= i1; i += kWarps) {
+            const float *part = p.part + (2 * static_cast<int64_t>(i) + (range_start(units, ctas, i) >= first ? 0 : 1)) * size;
+            const float mi = part[p.per_vhead * p.head_dim + 2 * h], li = part[p.per_vhead * p.head_dim + 2 * h + 1];
+            const float x = fmaxf(top, mi), z = x == -INFINITY ? 0.0f : x;
+            const float f = exp2_fast(top - z), fi = exp2_fast(mi - z);
+            sum = sum * f + li * fi;
+            top = x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = lane + 32 * j;
+                if (d < p.head_dim) o[j] = o[j] * f + part[h * p.head_dim + d] * fi;
+            }
+        }
+        if (lane == 0) {
+            s_top[warp] = top;
+            s_sum[warp] = sum;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_o[warp][lane + 32 * j] = o[j];
+        __syncthreads();
+        float x = s_top[0];
+        for (int i = 1; i < kWarps; ++i) x = fmaxf(x, s_top[i]);
+        const float z = x == -INFINITY ? 0.0f : x;
+        float f[kWarps], all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            f[i] = exp2_fast(s_top[i] - z);
+            all += f[i] * s_sum[i];
+        }
+        const float inv = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);
+        const int64_t head = head0 + h;
+        for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
+            float y = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) y += f[i] * s_o[i][d];
+            y *= inv;
+            if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(y);
+            else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = y;
+        }
+        if (p.lse && threadIdx.x == 0) p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (x + log2f(all)) * 0.6931471805599453f;
+        __syncthreads();
+    }
+}
+
+int per_vhead_of(int64_t group, int64_t head_dim) {
+    const int most = head_dim <= 128 ? 16 : 8;   // accumulators of 16 heads x 256 features do not fit the registers
+    return static_cast<int>(group < most ? group : most);
+}
+
+template <int DB, int NT, int ST>
+cudaError_t go(AttnParams p, int64_t most_units, cudaStream_t s) {
+    constexpr int smem = kWarps * ST * (64 * DB / 16) * 512;
+    static_assert(ST >= NT && smem <= 227 * 1024, "the ring holds the join of the warps");
+    const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, ST>);
+    cudaError_t e = smem_attr(f, smem);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> occupancy{0};   // the same on every device of this architecture
+    int occ = occupancy.load(std::memory_order_relaxed);
+    if (occ == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_paged_attn<DB, NT, ST>, kWarps * 32, smem);
+        if (e != cudaSuccess) return e;
+        if (occ < 1) occ = 1;
+        if (occ > kAttnMaxCtas) occ = kAttnMaxCtas;
+        occupancy.store(occ, std::memory_order_relaxed);
+    }
+    const int64_t room = static_cast<int64_t>(num_sms()) * occ;
+    p.grid = static_cast<int>(most_units < room ? most_units : room);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, ST>, p);
+    if (e != cudaSuccess) return e;
+    if ((p.max_pages << p.page_shift) <= kUnit) return cudaSuccess;   // one unit per head at most: nothing to join
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.n_seqs) * p.vheads));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_paged_attn_join, p);
+}
+
+}  // namespace
+
+size_t paged_attn_ws_bytes(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
+    if (n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 256;
+    const int64_t ctas = static_cast<int64_t>(num_sms()) * kAttnMaxCtas;
+    return 256 + static_cast<size_t>(2 * ctas * part_floats(per_vhead_of(n_heads / n_kv_heads, head_dim), static_cast<int>(head_dim))) * 4;
+}
+
+cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const KvCacheHost &c,
+                              const int32_t *pages, int64_t max_pages, const int32_t *lens, float scale, void *O, bool o_bf16,
+                              int64_t ldo, float *lse, void *ws, cudaStream_t s) {
+    AttnParams p = {};
+    p.q = static_cast<const __nv_bfloat16 *>(Q); p.ldq = ldq;
+    p.k = static_cast<const __nv_bfloat16 *>(c.k); p.v = static_cast<const __nv_bfloat16 *>(c.v);
+    p.page_stride = c.page_stride; p.head_stride = c.head_stride; p.row_stride = c.row_stride;
+    p.pages = pages; p.max_pages = max_pages; p.n_pages = c.n_pages; p.page_shift = c.page_shift; p.lens = lens;
+    p.n_seqs = static_cast<int>(n_seqs); p.n_heads = static_cast<int>(n_heads);
+    p.group = static_cast<int>(n_heads / c.n_kv_heads);
+    p.per_vhead = per_vhead_of(p.group, c.head_dim);
+    p.vper = (p.group + p.per_vhead - 1) / p.per_vhead;
+    p.vheads = c.n_kv_heads * p.vper;
+    p.head_dim = c.head_dim;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.o = O; p.o_bf16 = o_bf16 ? 1 : 0; p.ldo = ldo; p.lse = lse;
+    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+    p.status = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kStatusOffset);
+    const int64_t most_units = (((max_pages << c.page_shift) + kUnit - 1) / kUnit) * n_seqs * p.vheads;
+    const bool two = p.per_vhead > 8;
+    if (c.head_dim <= 64) return two ? go<1, 2, 4>(p, most_units, s) : go<1, 1, 4>(p, most_units, s);
+    if (c.head_dim <= 128) return two ? go<2, 2, 4>(p, most_units, s) : go<2, 1, 4>(p, most_units, s);
+    return go<4, 1, 3>(p, most_units, s);
+}
+
+}  // namespace bitnet

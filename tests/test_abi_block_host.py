@@ -124,3 +124,22 @@ def test_rope_append_refusals(lib):
     assert call(f, ok, ws=None) == WORKSPACE and call(f, ok, ws_bytes=0) == WORKSPACE
     assert call(f, ok, T=0, QKV=None, pos=None, Q=None) == _abi.BITNET_OK
     assert call(f, ok, T=0, rot_dim=0, table=None, n_pos=0) == _abi.BITNET_OK
+
+
+def test_paged_attn_refusals(lib):
+    f = lib.bitnet_paged_attn
+    need = lib.bitnet_paged_attn_workspace_size(4, 20, 5, 128)
+    ok = dict(Q=at(1), ldq=2560, n_seqs=4, n_heads=20, cache=cache(), pages=at(2), max_pages=8, lens=at(3), scale=0.1,
+              O=at(4), o_dtype=1, ldo=2560, lse=at(5), ws=at(6), ws_bytes=need, stream=None)
+    for name in ("Q", "pages", "lens", "O", "cache"):
+        assert call(f, ok, **{name: None}) == INVALID, name
+    for field, value, status in BAD_CACHES:
+        assert call(f, ok, cache=cache(**{field: value})) == status, field
+    for name, bad in (("ldq", 2559), ("ldo", 2559), ("n_seqs", -1), ("n_heads", 0), ("n_heads", 18), ("max_pages", 0),
+                      ("o_dtype", 2), ("scale", float("nan")), ("scale", float("inf")), ("O", at(1, 512)), ("Q", at(1, 1)),
+                      ("lens", at(3, 2)), ("ws", at(6, 8))):
+        assert call(f, ok, **{name: bad}) == INVALID, name
+    assert call(f, ok, max_pages=(1 << 26) + 1) == UNSUPPORTED       # 2^30 keys of pages of 16
+    assert call(f, ok, n_seqs=(1 << 20) + 1) == UNSUPPORTED
+    assert call(f, ok, ws=None) == WORKSPACE and call(f, ok, ws_bytes=need - 1) == WORKSPACE
+    assert call(f, ok, n_seqs=0, Q=None, O=None, pages=None, lens=None) == _abi.BITNET_OK
