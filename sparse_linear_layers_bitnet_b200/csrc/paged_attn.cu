@@ -6,15 +6,16 @@
 //
 // Bound: HBM.  Every key and value is read once and used for the few query
 // heads that share it, a handful of operations per byte.  So:
-//  * The work of a call, in units of 64 keys of one key-value head, is cut into
+//  * The work of a call, in units of 128 keys of one key-value head, is cut into
 //    one equal contiguous range per CTA (whatever the lengths are), and a CTA
 //    writes an unnormalised partial (m, sum, o) for a head whose keys it holds
 //    only a part of; a second small launch joins those.  The cut depends only
 //    on the lengths, so results repeat bit for bit.
-//  * Each of a CTA's four warps takes 16 keys of a unit.  A lane copies the
-//    16-byte pieces that it will itself use into its own shared-memory slots
-//    (cp.async, several pieces of 4 KB per warp in flight) and reads them back
-//    from there: no barrier, no bank conflict, no fragment shuffle.
+//  * Each of a CTA's four warps takes 32 keys of a unit (16 at 256 features).  A
+//    lane copies the 16-byte pieces that it will itself use into its own
+//    shared-memory slots (cp.async, two or three pieces of 8 KB per warp in
+//    flight) and reads them back from there: no barrier, no bank conflict, no
+//    fragment shuffle.
 //  * Products on mma.sync m16n8k16 with 16 keys (or 16 features of the values)
 //    as rows and 8 query heads as columns: S^T = K Q^T, then O^T += V^T P^T.
 //    The contraction index may be permuted at will, so K's fragments are the 16
@@ -33,7 +34,6 @@ namespace bitnet {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnit = 16 * kWarps;   // keys per unit
 
 struct AttnParams {
     const __nv_bfloat16 *q;
@@ -54,6 +54,8 @@ struct AttnParams {
     float *lse;                       // or NULL
     float *part;                      // [grid, 2] partials
     uint32_t *status;
+    int unit;                         // keys per unit
+    int q_vec;                        // Q's rows and heads lie on 16 bytes
     int grid;                         // CTAs of the first launch (those behind the number of units stay idle)
 };
 
@@ -103,31 +105,46 @@ __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
     return static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
 }
 __device__ __forceinline__ int64_t units_of(const AttnParams &p, int b) {
-    return static_cast<int64_t>((length_of(p, b) + kUnit - 1) / kUnit) * p.vheads;
+    return static_cast<int64_t>((length_of(p, b) + p.unit - 1) / p.unit) * p.vheads;
 }
 
-// Sum of units over the sequences below `upto` (exclusive), by the whole CTA of 128 threads.
-__device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *s_warp) {
-    int64_t s = 0;
-    for (int b = threadIdx.x; b < upto; b += blockDim.x) s += units_of(p, b);
+// Totals over the sequences, by the whole CTA of 128 threads: the units of all, and of those before sequence `upto`.
+__device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *before, int64_t *s_warp) {
+    int64_t all = 0, pre = 0;
+    for (int b = threadIdx.x; b < p.n_seqs; b += kWarps * 32) {
+        const int64_t n = units_of(p, b);
+        all += n;
+        if (b < upto) pre += n;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        pre += __shfl_xor_sync(0xffffffffu, pre, o);
+    }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = s;
+    if ((threadIdx.x & 31) == 0) {
+        s_warp[threadIdx.x >> 5] = all;
+        s_warp[kWarps + (threadIdx.x >> 5)] = pre;
+    }
     __syncthreads();
-    s = 0;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += s_warp[i];
-    return s;
+    all = pre = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        all += s_warp[i];
+        pre += s_warp[kWarps + i];
+    }
+    *before = pre;
+    return all;
 }
 
-// The sequence that holds unit u, and the units before it: the CTA scans blockDim.x sequences at a time.
+// The sequence that holds unit u, and the units before it (*first): the CTA scans 128 sequences at a time.
 __device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t *s_scan, int *s_at) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t before = 0;
-    for (int b0 = 0; b0 < p.n_seqs; b0 += blockDim.x) {
+    for (int b0 = 0; b0 < p.n_seqs; b0 += kWarps * 32) {
         const int b = b0 + threadIdx.x;
         const int64_t mine = b < p.n_seqs ? units_of(p, b) : 0;
         int64_t s = mine;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
@@ -138,7 +155,8 @@ __device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t 
         if (lane == 31) s_scan[warp] = s;
         __syncthreads();
         int64_t all = 0, base = before;
-        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) {
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
             if (i < warp) base += s_scan[i];
             all += s_scan[i];
         }
@@ -160,19 +178,24 @@ __device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t 
 // first unit of CTA i's range
 __device__ __forceinline__ int64_t range_start(int64_t units, int ctas, int i) { return units * i / ctas; }
 
-// floats of one partial: per query head head_dim of o, then m and the sum
-__host__ __device__ __forceinline__ int64_t part_floats(int per_vhead, int head_dim) {
-    return static_cast<int64_t>(per_vhead) * (head_dim + 2);
+// floats of one partial: per query head o in a row of head_dim rounded up to 4, then m and the sum of each
+__host__ __device__ __forceinline__ int part_row(int head_dim) { return (head_dim + 3) & ~3; }
+__host__ __device__ __forceinline__ int part_floats(int per_vhead, int head_dim) {
+    return (per_vhead * (part_row(head_dim) + 2) + 3) & ~3;
 }
 
-// DB: 64-feature blocks (head_dim <= 64 DB), NT: tiles of 8 query heads, ST: pieces a warp has in its ring
-template <int DB, int NT, int ST>
-__global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) {
+// DB: 64-feature blocks (head_dim <= 64 DB), NT: tiles of 8 query heads, KT: keys a warp takes at once (16 or 32),
+// ST: pieces (K or V of KT keys) in a warp's ring, FULL: head_dim is 64 DB
+template <int DB, int NT, int KT, int ST, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams p) {
     constexpr int D = 64 * DB;
-    constexpr int kPieces = D / 16;               // 16-byte pieces per lane of one tile (16 keys x D features)
-    constexpr uint32_t kTile = kPieces * 512;     // bytes of one tile
+    constexpr int R = KT / 8;                       // groups of 8 keys: a page holds whole groups
+    constexpr int M = KT / 16;                      // MMA row tiles
+    constexpr int kUnit = KT * kWarps;
+    constexpr uint32_t kPiece = KT * D * 2;         // bytes
+    constexpr uint32_t kAll = (1u << R) - 1;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t s_scan[kWarps + 1];
+    __shared__ int64_t s_scan[2 * kWarps];
     __shared__ int s_at;
     __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -184,25 +207,26 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
         const int n = __ldg(p.lens + b);
         if (threadIdx.x == 0 && (n < 0 || n > (p.max_pages << p.page_shift))) atomicOr(p.status, kStatusBadIndex);
         if (n > 0) continue;
-        for (int i = threadIdx.x; i < p.n_heads * p.head_dim; i += blockDim.x) {
+        for (int i = threadIdx.x; i < p.n_heads * p.head_dim; i += kWarps * 32) {
             if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + i] = __float2bfloat16_rn(0.0f);
             else static_cast<float *>(p.o)[b * p.ldo + i] = 0.0f;
         }
         if (p.lse)
-            for (int i = threadIdx.x; i < p.n_heads; i += blockDim.x)
+            for (int i = threadIdx.x; i < p.n_heads; i += kWarps * 32)
                 p.lse[static_cast<int64_t>(b) * p.n_heads + i] = -INFINITY;
     }
 
-    const int64_t units = sum_units(p, p.n_seqs, s_scan);
+    int64_t first = 0;
+    const int64_t units = sum_units(p, 0, &first, s_scan);
     const int ctas = static_cast<int>(units < p.grid ? units : p.grid);   // every one of them gets a unit
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     const int64_t lo = range_start(units, ctas, blockIdx.x), hi = range_start(units, ctas, blockIdx.x + 1);
-    int64_t first = 0;
     int b = find_seq(p, lo, &first, s_scan, &s_at);
 
-    const uint32_t ring = smem_u32(smem) + warp * (ST * kTile) + lane * 16;
-    // words of the last 16-byte piece of a row that hold features (head_dim not a multiple of 8)
+    const uint32_t ring = smem_u32(smem) + warp * (ST * kPiece) + lane * 16;
+    // the 16-byte pieces of a row that hold features; the last one may hold fewer than 8
     const int last_piece = (p.head_dim - 1) >> 3, tail = p.head_dim - 8 * last_piece;
+    const int row_mask = (1 << p.page_shift) - 1;
 
     int64_t u = lo;
     while (u < hi) {
@@ -219,6 +243,90 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
         const int kvh = vh / p.vper, head0 = kvh * p.group + (vh % p.vper) * p.per_vhead;
         const int heads = min(p.per_vhead, (kvh + 1) * p.group - head0);
 
+        // this warp's tiles: KT keys from key0, + kUnit, ...
+        const int key0 = static_cast<int>((u - seg_first) * kUnit) + KT * warp;
+        const int key_end = min(len, static_cast<int>((end - seg_first) * kUnit));
+        const int tiles = key_end > key0 ? (key_end - key0 + kUnit - 1) / kUnit : 0;
+        const int32_t *list = p.pages + b * p.max_pages;
+        const __nv_bfloat16 *kl = p.k + kvh * p.head_stride + g * p.row_stride + 8 * t;
+        const __nv_bfloat16 *vl = p.v + kvh * p.head_stride + 2 * t * p.row_stride + 8 * g;
+
+        // the pages of the next tile to be copied are loaded one tile ahead
+        int next[R];
+        auto look_up = [&](int key) {
+            next[0] = key < key_end ? __ldg(list + (key >> p.page_shift)) : -1;
+            if ((KT - 1) >> p.page_shift) {   // pages smaller than a tile
+#pragma unroll
+                for (int r = 1; r < R; ++r) next[r] = key + 8 * r < key_end ? __ldg(list + ((key + 8 * r) >> p.page_shift)) : -1;
+            } else {
+#pragma unroll
+                for (int r = 1; r < R; ++r) next[r] = next[0];
+            }
+        };
+        int64_t off[R];         // of the tile last begun: offset of each group's first row
+        uint32_t ok_bits = 0;   // 8 bits per tile in flight: its groups' pages are valid
+        int k_tile = 0, v_tile = 0, slot = 0;   // next tile to be copied, ring slot for it
+        auto issue_k = [&]() {
+            if (k_tile < tiles) {
+                const int key = key0 + k_tile * kUnit;
+                const uint32_t dst = ring + slot * kPiece;
+                uint32_t ok = 0;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const bool fine = next[r] >= 0 && next[r] < p.n_pages;
+                    ok |= fine ? 1u << r : 0u;
+                    off[r] = fine ? next[r] * p.page_stride + ((key + 8 * r) & row_mask) * p.row_stride : 0;
+                }
+                const bool all = ok == kAll && key + KT <= key_end;
+                if (!all && lane == 0) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (key + 8 * r < key_end && !(ok >> r & 1u)) atomicOr(p.status, kStatusBadIndex);
+                }
+                ok_bits = (ok_bits & ~(0xffu << (8 * (k_tile & 3)))) | (ok << (8 * (k_tile & 3)));
+                look_up(key + kUnit);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const bool in = all || ((ok >> r & 1u) && key + 8 * r + g < key_end);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const bool have = in && (FULL || 4 * i + t <= last_piece);
+                        cp16(dst + (r * (D / 32) + i) * 512, have ? kl + off[r] + 32 * i : p.k, have);
+                    }
+                }
+                ++k_tile;
+                slot = slot + 1 == ST ? 0 : slot + 1;
+            }
+            cp_commit();
+        };
+        auto issue_v = [&]() {
+            if (v_tile < tiles) {
+                const int key = key0 + v_tile * kUnit;
+                const uint32_t dst = ring + slot * kPiece;
+                const uint32_t ok = ok_bits >> (8 * (v_tile & 3)) & kAll;
+                const bool all = ok == kAll && key + KT <= key_end;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool in = all || ((ok >> r & 1u) && key + 8 * r + 2 * t + e < key_end);
+                        const __nv_bfloat16 *src = vl + off[r] + e * p.row_stride;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            const bool have = in && (FULL || 8 * d + g <= last_piece);
+                            cp16(dst + ((2 * r + e) * DB + d) * 512, have ? src + 64 * d : p.v, have);
+                        }
+                    }
+                ++v_tile;
+                slot = slot + 1 == ST ? 0 : slot + 1;
+            }
+            cp_commit();
+        };
+        look_up(key0);
+        issue_k();
+        issue_v();
+        if (ST == 4) issue_k();
+
         // Q fragments: column g of tile n is query head head0 + 8 n + g; piece i of lane (g, t) is
         // features 32 i + 8 t .. + 7, the same that the lane holds of a key
         uint4 qf[NT][D / 32];
@@ -228,12 +336,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
             for (int i = 0; i < D / 32; ++i) {
                 const int h = 8 * n + g, f = 32 * i + 8 * t;
                 uint32_t w[4] = {0u, 0u, 0u, 0u};
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + b * p.ldq +
+                                      static_cast<int64_t>(head0 + h) * p.head_dim + f;
                 if (h < heads) {
-                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + b * p.ldq +
-                                          static_cast<int64_t>(head0 + h) * p.head_dim;
+                    if (p.q_vec) {
+                        if (FULL || f < p.head_dim) {
+                            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        }
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (f + e < p.head_dim) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + f + e)) << (16 * (e & 1));
+                        for (int e = 0; e < 8; ++e)
+                            if (f + e < p.head_dim) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + e)) << (16 * (e & 1));
+                    }
                 }
                 qf[n][i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -252,112 +367,69 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
                     for (int c = 0; c < 4; ++c) o[n][d][w][c] = 0.0f;
         }
 
-        // this warp's tiles: 16 keys from key0, + 64, ...
-        const int key0 = static_cast<int>((u - seg_first) * kUnit) + 16 * warp;
-        const int key_end = min(len, static_cast<int>((end - seg_first) * kUnit));
-        const int tiles = key_end > key0 ? (key_end - key0 + kUnit - 1) / kUnit : 0;
-        const __nv_bfloat16 *kbase = p.k + kvh * p.head_stride, *vbase = p.v + kvh * p.head_stride;
-        const int32_t *list = p.pages + b * p.max_pages;
-
-        // pages of the 8-key halves of the next tile to be copied (a page holds at least 8 keys)
-        auto page_of = [&](int key) { return key < key_end ? __ldg(list + (key >> p.page_shift)) : -1; };
-        int issue_key = key0, issued = 0;
-        int next0 = page_of(key0), next1 = page_of(key0 + 8);
-        int cur0 = 0, cur1 = 0;
-        uint32_t ok_bits = 0;   // two bits per tile in flight: its halves' pages are valid
-        int slot = 0;           // ring slot of the next piece to be copied
-        auto issue = [&]() {    // copies the next tile of the sequence K0 V0 K1 V1 ...
-            if (issued < 2 * tiles) {
-                const uint32_t dst = ring + slot * kTile;
-                const int row_mask = (1 << p.page_shift) - 1;
-                if ((issued & 1) == 0) {
-                    cur0 = next0;
-                    cur1 = next1;
-                    const bool ok0 = cur0 >= 0 && cur0 < p.n_pages, ok1 = cur1 >= 0 && cur1 < p.n_pages;
-                    const int sh = 2 * ((issued >> 1) & 7);
-                    ok_bits = (ok_bits & ~(3u << sh)) | ((ok0 ? 1u : 0u) << sh) | ((ok1 ? 2u : 0u) << sh);
-                    if (lane == 0 && ((!ok0 && issue_key < key_end) || (!ok1 && issue_key + 8 < key_end)))
-                        atomicOr(p.status, kStatusBadIndex);
-                    next0 = page_of(issue_key + kUnit);
-                    next1 = page_of(issue_key + kUnit + 8);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int key = issue_key + 8 * r + g;
-                        const bool in = key < key_end && (r ? ok1 : ok0);
-                        const __nv_bfloat16 *src = kbase + (in ? (r ? cur1 : cur0) * p.page_stride + (key & row_mask) * p.row_stride : 0);
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            const int piece = 4 * i + t;
-                            const bool have = in && piece <= last_piece;
-                            cp16(dst + (r * (D / 32) + i) * 512, src + (have ? 8 * piece : 0), have);
-                        }
-                    }
-                } else {
-                    const int sh = 2 * ((issued >> 1) & 7);
-                    const bool ok0 = (ok_bits >> sh) & 1u, ok1 = (ok_bits >> sh) & 2u;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int key = issue_key + 8 * (r >> 1) + 2 * t + (r & 1);
-                        const bool in = key < key_end && ((r >> 1) ? ok1 : ok0);
-                        const __nv_bfloat16 *src = vbase + (in ? ((r >> 1) ? cur1 : cur0) * p.page_stride + (key & row_mask) * p.row_stride : 0);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            const int piece = 8 * d + g;
-                            const bool have = in && piece <= last_piece;
-                            cp16(dst + (r * DB + d) * 512, src + (have ? 8 * piece : 0), have);
-                        }
-                    }
-                    issue_key += kUnit;
-                }
-                ++issued;
-                slot = slot + 1 == ST ? 0 : slot + 1;
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < ST - 1; ++i) issue();
-
         int use = 0;   // ring slot of the next piece to be used
         for (int tile = 0; tile < tiles; ++tile) {
-            // S^T = K Q^T: rows are keys g and g + 8, columns the heads 2 t and 2 t + 1 of each tile
+            // S^T = K Q^T: rows g and g + 8 of row tile k are keys 16 k + g and 16 k + 8 + g, columns the
+            // heads 2 t and 2 t + 1 of each tile of 8
             cp_wait<ST - 2>();
-            float s[NT][4];
+            float s[NT][M][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < M; ++k) s[n][k][0] = s[n][k][1] = s[n][k][2] = s[n][k][3] = 0.0f;
             {
-                const uint32_t src = ring + use * kTile;
+                const uint32_t src = ring + use * kPiece;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint4 a = lds16(src + i * 512), c = lds16(src + (D / 32 + i) * 512);
-                    if (tail < 8 && 4 * i + t == last_piece) {   // what lies behind head_dim may be anything
-                        uint32_t *aw = reinterpret_cast<uint32_t *>(&a), *cw = reinterpret_cast<uint32_t *>(&c);
+                for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t keep = tail >= 2 * e + 2 ? 0xffffffffu : tail == 2 * e + 1 ? 0xffffu : 0u;
-                            aw[e] &= keep;
-                            cw[e] &= keep;
+                    for (int k = 0; k < M; ++k) {
+                        uint4 a = lds16(src + (2 * k * (D / 32) + i) * 512), c = lds16(src + ((2 * k + 1) * (D / 32) + i) * 512);
+                        if (!FULL && tail < 8 && 4 * i + t == last_piece) {   // what lies behind head_dim may be anything
+                            const uint32_t k0 = tail >= 2 ? 0xffffffffu : 0xffffu, k1 = tail >= 4 ? 0xffffffffu : tail == 3 ? 0xffffu : 0u;
+                            const uint32_t k2 = tail >= 6 ? 0xffffffffu : tail == 5 ? 0xffffu : 0u, k3 = tail == 7 ? 0xffffu : 0u;
+                            a = make_uint4(a.x & k0, a.y & k1, a.z & k2, a.w & k3);
+                            c = make_uint4(c.x & k0, c.y & k1, c.z & k2, c.w & k3);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma(s[n][k], a.x, c.x, a.y, c.y, qf[n][i].x, qf[n][i].y);
+                            mma(s[n][k], a.z, c.z, a.w, c.w, qf[n][i].z, qf[n][i].w);
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma(s[n], a.x, c.x, a.y, c.y, qf[n][i].x, qf[n][i].y);
-                        mma(s[n], a.z, c.z, a.w, c.w, qf[n][i].z, qf[n][i].w);
-                    }
-                }
             }
             use = use + 1 == ST ? 0 : use + 1;
-            issue();
+            if (ST == 4) issue_v(); else issue_k();
 
             // mask, running maximum, p
-            const int key = key0 + tile * kUnit + g;
-            const uint32_t okb = ok_bits >> (2 * (tile & 7));
-            const bool in0 = key < key_end && (okb & 1u), in1 = key + 8 < key_end && (okb & 2u);
-            uint32_t ph[NT][2], pl[NT][2];
+            const int key = key0 + tile * kUnit;
+            const uint32_t ok = ok_bits >> (8 * (tile & 3)) & kAll;
+            if (ok != kAll || key + KT > key_end) {
+#pragma unroll
+                for (int k = 0; k < M; ++k) {
+                    const bool in0 = (ok >> (2 * k) & 1u) && key + 16 * k + g < key_end;
+                    const bool in1 = (ok >> (2 * k + 1) & 1u) && key + 16 * k + 8 + g < key_end;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[n][k][c] = (c < 2 ? in0 : in1) ? s[n][k][c] * p.scale_log2 : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < M; ++k)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[n][k][c] *= p.scale_log2;
+            }
+            uint32_t ph[NT][M][2], pl[NT][M][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                float x0 = fmaxf(s[n][0][0], s[n][0][2]), x1 = fmaxf(s[n][0][1], s[n][0][3]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[n][c] = (c < 2 ? in0 : in1) ? s[n][c] * p.scale_log2 : -INFINITY;
-                float x0 = fmaxf(s[n][0], s[n][2]), x1 = fmaxf(s[n][1], s[n][3]);
+                for (int k = 1; k < M; ++k) {
+                    x0 = fmaxf(x0, fmaxf(s[n][k][0], s[n][k][2]));
+                    x1 = fmaxf(x1, fmaxf(s[n][k][1], s[n][k][3]));
+                }
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) {
                     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
@@ -383,44 +455,52 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
                     m[n][1] = m1;
                 }
                 const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-                const float p0 = exp2_fast(s[n][0] - z0), p1 = exp2_fast(s[n][1] - z1);
-                const float p2 = exp2_fast(s[n][2] - z0), p3 = exp2_fast(s[n][3] - z1);
-                l[n][0] += p0 + p2;
-                l[n][1] += p1 + p3;
-                split2(p0, p1, ph[n][0], pl[n][0]);
-                split2(p2, p3, ph[n][1], pl[n][1]);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    ph[n][r] = transpose8x8(ph[n][r]);
-                    pl[n][r] = transpose8x8(pl[n][r]);
+                for (int k = 0; k < M; ++k) {
+                    const float p0 = exp2_fast(s[n][k][0] - z0), p1 = exp2_fast(s[n][k][1] - z1);
+                    const float p2 = exp2_fast(s[n][k][2] - z0), p3 = exp2_fast(s[n][k][3] - z1);
+                    l[n][0] += p0 + p2;
+                    l[n][1] += p1 + p3;
+                    split2(p0, p1, ph[n][k][0], pl[n][k][0]);
+                    split2(p2, p3, ph[n][k][1], pl[n][k][1]);
                 }
+#pragma unroll
+                for (int k = 0; k < M; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        ph[n][k][r] = transpose8x8(ph[n][k][r]);
+                        pl[n][k][r] = transpose8x8(pl[n][k][r]);
+                    }
             }
 
-            // O^T += V^T P^T: lane (g, t) holds features 64 d + 8 g .. + 7 of keys 2t, 2t+1, 2t+8, 2t+9
+            // O^T += V^T P^T: of row tile k, lane (g, t) holds features 64 d + 8 g .. + 7 of keys
+            // 16 k + 2t, 2t + 1, 2t + 8 and 2t + 9
             cp_wait<ST - 2>();
             {
-                const uint32_t src = ring + use * kTile;
+                const uint32_t src = ring + use * kPiece;
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const uint4 v0 = lds16(src + d * 512), v1 = lds16(src + (DB + d) * 512);
-                    const uint4 v2 = lds16(src + (2 * DB + d) * 512), v3 = lds16(src + (3 * DB + d) * 512);
-                    const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-                    const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+                for (int k = 0; k < M; ++k)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
-                        const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
-                        const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+                    for (int d = 0; d < DB; ++d) {
+                        const uint4 v0 = lds16(src + ((4 * k) * DB + d) * 512), v1 = lds16(src + ((4 * k + 1) * DB + d) * 512);
+                        const uint4 v2 = lds16(src + ((4 * k + 2) * DB + d) * 512), v3 = lds16(src + ((4 * k + 3) * DB + d) * 512);
+                        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                        const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma(o[n][d][w], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-                            mma(o[n][d][w], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                        for (int w = 0; w < 4; ++w) {
+                            // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
+                            const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
+                            const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma(o[n][d][w], a0, a1, a2, a3, ph[n][k][0], ph[n][k][1]);
+                                mma(o[n][d][w], a0, a1, a2, a3, pl[n][k][0], pl[n][k][1]);
+                            }
                         }
                     }
-                }
             }
             use = use + 1 == ST ? 0 : use + 1;
-            issue();
+            if (ST == 4) issue_k(); else issue_v();
         }
         cp_wait<0>();
 
@@ -434,24 +514,26 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
                 l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], w);
                 l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], w);
             }
-            if (g == 0) {
-                s_m[warp][8 * n + 2 * t] = m[n][0];
-                s_m[warp][8 * n + 2 * t + 1] = m[n][1];
-                s_l[warp][8 * n + 2 * t] = l[n][0];
-                s_l[warp][8 * n + 2 * t + 1] = l[n][1];
-            }
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+            for (int c = 0; c < 2; ++c) {
+                const int h = 8 * n + 2 * t + c;
+                if (h >= heads) continue;
+                if (g == 0) {
+                    s_m[warp][h] = m[n][c];
+                    s_l[warp][h] = l[n][c];
+                }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float4 *dst = reinterpret_cast<float4 *>(s_o + (warp * 8 * NT + 8 * n + 2 * t + c) * D + 64 * d + 8 * g);
+                for (int d = 0; d < DB; ++d) {
+                    float4 *dst = reinterpret_cast<float4 *>(s_o + (warp * 8 * NT + h) * D + 64 * d + 8 * g);
                     dst[0] = make_float4(o[n][d][0][c], o[n][d][0][2 + c], o[n][d][1][c], o[n][d][1][2 + c]);
                     dst[1] = make_float4(o[n][d][2][c], o[n][d][2][2 + c], o[n][d][3][c], o[n][d][3][2 + c]);
                 }
+            }
         }
         __syncthreads();
         const bool whole = u == seg_first && end == seg_end;
         float *part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (u == lo ? 0 : 1)) * part_floats(p.per_vhead, p.head_dim);
+        const int row = part_row(p.head_dim);
         for (int h = warp; h < heads; h += kWarps) {
             float top = s_m[0][h];
 #pragma unroll
@@ -470,14 +552,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) x += f[i] * s_o[(i * 8 * NT + h) * D + d];
                 x *= inv;
-                if (!whole) part[h * p.head_dim + d] = x;
+                if (!whole) part[h * row + d] = x;
                 else if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(x);
                 else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = x;
             }
             if (lane == 0) {
                 if (!whole) {
-                    part[p.per_vhead * p.head_dim + 2 * h] = top;
-                    part[p.per_vhead * p.head_dim + 2 * h + 1] = sum;
+                    part[p.per_vhead * row + 2 * h] = top;
+                    part[p.per_vhead * row + 2 * h + 1] = sum;
                 } else if (p.lse) {
                     p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
                 }
@@ -488,74 +570,101 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(const AttnParams p) 
     }
 }
 
-// Joins the partials of the heads that more than one CTA of the first launch worked on: CTA (b, virtual head).
-__global__ void __launch_bounds__(128) k_paged_attn_join(const AttnParams p) {
-    __shared__ int64_t s_warp[kWarps + 1];
+// Joins the partials of the heads that more than one CTA of the first launch worked on: CTA (query head, sequence).
+// A warp takes every fourth partial, 32 of them at a time: lane j holds the j-th one's maximum and sum.
+__global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParams p) {
+    __shared__ int64_t s_warp[2 * kWarps];
     __shared__ float s_top[kWarps], s_sum[kWarps];
-    __shared__ float s_o[kWarps][256];
+    __shared__ float4 s_o[kWarps][64];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x / p.vheads, vh = blockIdx.x % p.vheads;
-    const int len = length_of(p, b);
-    const int64_t n_units = (len + kUnit - 1) / kUnit;
+    const int b = blockIdx.x / p.n_heads, head = blockIdx.x % p.n_heads;
+    const int64_t n_units = (length_of(p, b) + p.unit - 1) / p.unit;
     if (n_units < 2) return;
-    const int64_t units = sum_units(p, p.n_seqs, s_warp);
-    const int64_t first = sum_units(p, b, s_warp) + vh * n_units, end = first + n_units;
+    const int kvh = head / p.group, in_group = head % p.group;
+    const int vh = kvh * p.vper + in_group / p.per_vhead, h = in_group % p.per_vhead;
+    int64_t first;
+    const int64_t units = sum_units(p, b, &first, s_warp);
+    first += vh * n_units;
+    const int64_t end = first + n_units;
     // CTA of unit u: the largest i with range_start(i) <= u
     const int ctas = static_cast<int>(units < p.grid ? units : p.grid);
     const int i0 = static_cast<int>(((first + 1) * ctas - 1) / units), i1 = static_cast<int>((end * ctas - 1) / units);
     if (i0 == i1) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = vh / p.vper, head0 = kvh * p.group + (vh % p.vper) * p.per_vhead;
-    const int heads = min(p.per_vhead, (kvh + 1) * p.group - head0);
     const int64_t size = part_floats(p.per_vhead, p.head_dim);
-    for (int h = 0; h < heads; ++h) {
-        // each warp joins every fourth partial, then the four are joined
-        float top = -INFINITY, sum = 0.0f, o[8];
+    const int row = part_row(p.head_dim);
+    // partial i: in slot 0 when the range begins inside the head's keys, else (only i0 can) in slot 1
+    auto partial = [&](int i) { return p.part + (2 * static_cast<int64_t>(i) + (i == i0 && range_start(units, ctas, i) < first ? 1 : 0)) * size; };
+    float top = -INFINITY, sum = 0.0f;
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int j0 = i0 + warp; j0 <= i1; j0 += kWarps * 32) {
+        const int mine = j0 + kWarps * lane;
+        float mi = -INFINITY, li = 0.0f;
+        if (mine <= i1) {
+            const float *ml = partial(mine) + p.per_vhead * row + 2 * h;
+            mi = ml[0];
+            li = ml[1];
+        }
+        float x = fmaxf(top, mi);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-        for (int i = i0 + warp; i <= i1; i += kWarps) {
-            const float *part = p.part + (2 * static_cast<int64_t>(i) + (range_start(units, ctas, i) >= first ? 0 : 1)) * size;
-            const float mi = part[p.per_vhead * p.head_dim + 2 * h], li = part[p.per_vhead * p.head_dim + 2 * h + 1];
-            const float x = fmaxf(top, mi), z = x == -INFINITY ? 0.0f : x;
-            const float f = exp2_fast(top - z), fi = exp2_fast(mi - z);
-            sum = sum * f + li * fi;
-            top = x;
+        for (int w = 16; w > 0; w >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+        const float z = x == -INFINITY ? 0.0f : x;
+        const float f = exp2_fast(top - z), fi = exp2_fast(mi - z);
+        float si = li * fi;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d = lane + 32 * j;
-                if (d < p.head_dim) o[j] = o[j] * f + part[h * p.head_dim + d] * fi;
+        for (int w = 16; w > 0; w >>= 1) si += __shfl_xor_sync(0xffffffffu, si, w);
+        sum = sum * f + si;
+        top = x;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            o[c].x *= f; o[c].y *= f; o[c].z *= f; o[c].w *= f;
+        }
+        const int n = min(32, (i1 - j0) / kWarps + 1);
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const float fj = __shfl_sync(0xffffffffu, fi, j);
+            const float4 *src = reinterpret_cast<const float4 *>(partial(j0 + kWarps * j) + h * row);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (4 * (lane + 32 * c) < row) {
+                    const float4 v = src[lane + 32 * c];
+                    o[c].x = fmaf(v.x, fj, o[c].x);
+                    o[c].y = fmaf(v.y, fj, o[c].y);
+                    o[c].z = fmaf(v.z, fj, o[c].z);
+                    o[c].w = fmaf(v.w, fj, o[c].w);
+                }
             }
         }
-        if (lane == 0) {
-            s_top[warp] = top;
-            s_sum[warp] = sum;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s_o[warp][lane + 32 * j] = o[j];
-        __syncthreads();
-        float x = s_top[0];
-        for (int i = 1; i < kWarps; ++i) x = fmaxf(x, s_top[i]);
-        const float z = x == -INFINITY ? 0.0f : x;
-        float f[kWarps], all = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            f[i] = exp2_fast(s_top[i] - z);
-            all += f[i] * s_sum[i];
-        }
-        const float inv = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);
-        const int64_t head = head0 + h;
-        for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
-            float y = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) y += f[i] * s_o[i][d];
-            y *= inv;
-            if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(y);
-            else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = y;
-        }
-        if (p.lse && threadIdx.x == 0) p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (x + log2f(all)) * 0.6931471805599453f;
-        __syncthreads();
     }
+    if (lane == 0) {
+        s_top[warp] = top;
+        s_sum[warp] = sum;
+    }
+    s_o[warp][lane] = o[0];
+    s_o[warp][lane + 32] = o[1];
+    __syncthreads();
+    float x = s_top[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) x = fmaxf(x, s_top[i]);
+    const float z = x == -INFINITY ? 0.0f : x;
+    float f[kWarps], all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        f[i] = exp2_fast(s_top[i] - z);
+        all += f[i] * s_sum[i];
+    }
+    const float inv = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);
+    for (int d = threadIdx.x; d < p.head_dim; d += kWarps * 32) {
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) y += f[i] * reinterpret_cast<const float *>(s_o[i])[d];
+        y *= inv;
+        const int64_t at = b * p.ldo + static_cast<int64_t>(head) * p.head_dim + d;
+        if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[at] = __float2bfloat16_rn(y);
+        else static_cast<float *>(p.o)[at] = y;
+    }
+    if (p.lse && threadIdx.x == 0) p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (x + log2f(all)) * 0.6931471805599453f;
 }
 
 int per_vhead_of(int64_t group, int64_t head_dim) {
@@ -563,24 +672,26 @@ int per_vhead_of(int64_t group, int64_t head_dim) {
     return static_cast<int>(group < most ? group : most);
 }
 
-template <int DB, int NT, int ST>
-cudaError_t go(AttnParams p, int64_t most_units, cudaStream_t s) {
-    constexpr int smem = kWarps * ST * (64 * DB / 16) * 512;
-    static_assert(ST >= NT && smem <= 227 * 1024, "the ring holds the join of the warps");
-    const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, ST>);
+template <int DB, int NT, int KT, int ST, bool FULL>
+cudaError_t go(AttnParams p, cudaStream_t s) {
+    constexpr int smem = kWarps * ST * KT * 64 * DB * 2;
+    static_assert(ST * KT * 2 >= 8 * NT * 4 && smem <= 227 * 1024, "the ring holds the join of the warps");
+    const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, KT, ST, FULL>);
     cudaError_t e = smem_attr(f, smem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> occupancy{0};   // the same on every device of this architecture
     int occ = occupancy.load(std::memory_order_relaxed);
     if (occ == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_paged_attn<DB, NT, ST>, kWarps * 32, smem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_paged_attn<DB, NT, KT, ST, FULL>, kWarps * 32, smem);
         if (e != cudaSuccess) return e;
         if (occ < 1) occ = 1;
         if (occ > kAttnMaxCtas) occ = kAttnMaxCtas;
         occupancy.store(occ, std::memory_order_relaxed);
     }
+    p.unit = KT * kWarps;
+    const int64_t most = (((p.max_pages << p.page_shift) + p.unit - 1) / p.unit) * p.n_seqs * p.vheads;
     const int64_t room = static_cast<int64_t>(num_sms()) * occ;
-    p.grid = static_cast<int>(most_units < room ? most_units : room);
+    p.grid = static_cast<int>(most < room ? most : room);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -591,13 +702,21 @@ cudaError_t go(AttnParams p, int64_t most_units, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, ST>, p);
+    e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, KT, ST, FULL>, p);
     if (e != cudaSuccess) return e;
-    if ((p.max_pages << p.page_shift) <= kUnit) return cudaSuccess;   // one unit per head at most: nothing to join
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.n_seqs) * p.vheads));
-    cfg.blockDim = dim3(128);
+    if ((p.max_pages << p.page_shift) <= p.unit) return cudaSuccess;   // one unit per head at most: nothing to join
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.n_seqs) * p.n_heads));
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_paged_attn_join, p);
+}
+
+template <int DB, int KT, int ST>
+cudaError_t by_heads(const AttnParams &p, cudaStream_t s) {
+    const bool full = p.head_dim == 64 * DB;
+    if constexpr (DB < 4) {
+        if (p.per_vhead > 8) return full ? go<DB, 2, KT, ST, true>(p, s) : go<DB, 2, KT, ST, false>(p, s);
+    }
+    return full ? go<DB, 1, KT, ST, true>(p, s) : go<DB, 1, KT, ST, false>(p, s);
 }
 
 }  // namespace
@@ -605,7 +724,7 @@ cudaError_t go(AttnParams p, int64_t most_units, cudaStream_t s) {
 size_t paged_attn_ws_bytes(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
     if (n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 256;
     const int64_t ctas = static_cast<int64_t>(num_sms()) * kAttnMaxCtas;
-    return 256 + static_cast<size_t>(2 * ctas * part_floats(per_vhead_of(n_heads / n_kv_heads, head_dim), static_cast<int>(head_dim))) * 4;
+    return 256 + static_cast<size_t>(2 * ctas) * static_cast<size_t>(part_floats(per_vhead_of(n_heads / n_kv_heads, head_dim), static_cast<int>(head_dim))) * 4;
 }
 
 cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const KvCacheHost &c,
@@ -626,11 +745,11 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
     p.o = O; p.o_bf16 = o_bf16 ? 1 : 0; p.ldo = ldo; p.lse = lse;
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
     p.status = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kStatusOffset);
-    const int64_t most_units = (((max_pages << c.page_shift) + kUnit - 1) / kUnit) * n_seqs * p.vheads;
-    const bool two = p.per_vhead > 8;
-    if (c.head_dim <= 64) return two ? go<1, 2, 4>(p, most_units, s) : go<1, 1, 4>(p, most_units, s);
-    if (c.head_dim <= 128) return two ? go<2, 2, 4>(p, most_units, s) : go<2, 1, 4>(p, most_units, s);
-    return go<4, 1, 3>(p, most_units, s);
+    p.q_vec = c.head_dim % 8 == 0 && ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(Q) & 15) == 0;
+    // 32 keys at once and two to four CTAs per SM; at 256 features 16 keys, so that two CTAs fit
+    if (c.head_dim <= 64) return by_heads<1, 32, 4>(p, s);
+    if (c.head_dim <= 128) return by_heads<2, 32, 3>(p, s);
+    return by_heads<4, 16, 3>(p, s);
 }
 
 }  // namespace bitnet
