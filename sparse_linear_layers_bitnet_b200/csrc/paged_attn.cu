@@ -11,11 +11,12 @@
 //    writes an unnormalised partial (m, sum, o) for a head whose keys it holds
 //    only a part of; a second small launch joins those.  The cut depends only
 //    on the lengths, so results repeat bit for bit.
-//  * Each of a CTA's four warps takes 32 keys of a unit (16 at 256 features).  A
-//    lane copies the 16-byte pieces that it will itself use into its own
-//    shared-memory slots (cp.async, two or three pieces of 8 KB per warp in
-//    flight) and reads them back from there: no barrier, no bank conflict, no
-//    fragment shuffle.
+//  * Each of a CTA's four warps takes 32 keys of a unit (16 at 256 features).  They
+//    go through a ring of its own in shared memory (cp.async, two or three
+//    pieces of 8 KB per warp in flight), so warps wait for nobody but
+//    themselves.  Eight lanes copy 128 consecutive bytes: with each lane
+//    copying just what it will use (32- and 64-byte runs), L2 delivered every
+//    byte twice.
 //  * Products on mma.sync m16n8k16 with 16 keys (or 16 features of the values)
 //    as rows and 8 query heads as columns: S^T = K Q^T, then O^T += V^T P^T.
 //    The contraction index may be permuted at will, so K's fragments are the 16
@@ -223,10 +224,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     const int64_t lo = range_start(units, ctas, blockIdx.x), hi = range_start(units, ctas, blockIdx.x + 1);
     int b = find_seq(p, lo, &first, s_scan, &s_at);
 
-    const uint32_t ring = smem_u32(smem) + warp * (ST * kPiece) + lane * 16;
+    // The ring holds rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take a
+    // segment, 16 bytes each.  A 16-byte chunk j lies at j ^ 4 (r & 1) of its segment for K, j ^ (r & 6) for V, so
+    // that the eight lanes of a read phase (below) meet eight different chunks.
+    const uint32_t ring = smem_u32(smem) + warp * (ST * kPiece);
+    const int cq = lane >> 3, cj = lane & 7;   // copies: row of four, chunk
+    const uint32_t k_to = cq * DB * 128 + ((cj ^ (4 * (cq & 1))) << 4);
+    const uint32_t v_to = cq * DB * 128;       // + chunk, which depends on the row of eight
+    const uint32_t v_chunk0 = (cj ^ (cq & 2)) << 4, v_chunk1 = (cj ^ (4 + (cq & 2))) << 4;
+    const uint32_t k_from = g * DB * 128 + ((t ^ (4 * (g & 1))) << 4);   // chunk t; chunk 4 + t is at ^ 64
+    const uint32_t v_from = 2 * t * DB * 128 + ((g ^ (2 * t)) << 4);
     // the 16-byte pieces of a row that hold features; the last one may hold fewer than 8
     const int last_piece = (p.head_dim - 1) >> 3, tail = p.head_dim - 8 * last_piece;
     const int row_mask = (1 << p.page_shift) - 1;
+    const int64_t row4 = 4 * p.row_stride;
 
     int64_t u = lo;
     while (u < hi) {
@@ -248,8 +259,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         const int key_end = min(len, static_cast<int>((end - seg_first) * kUnit));
         const int tiles = key_end > key0 ? (key_end - key0 + kUnit - 1) / kUnit : 0;
         const int32_t *list = p.pages + b * p.max_pages;
-        const __nv_bfloat16 *kl = p.k + kvh * p.head_stride + g * p.row_stride + 8 * t;
-        const __nv_bfloat16 *vl = p.v + kvh * p.head_stride + 2 * t * p.row_stride + 8 * g;
+        const __nv_bfloat16 *kl = p.k + kvh * p.head_stride + cq * p.row_stride + 8 * cj;
+        const __nv_bfloat16 *vl = p.v + kvh * p.head_stride + cq * p.row_stride + 8 * cj;
 
         // the pages of the next tile to be copied are loaded one tile ahead
         int next[R];
@@ -286,12 +297,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 ok_bits = (ok_bits & ~(0xffu << (8 * (k_tile & 3)))) | (ok << (8 * (k_tile & 3)));
                 look_up(key + kUnit);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const bool in = all || ((ok >> r & 1u) && key + 8 * r + g < key_end);
+                for (int h = 0; h < 2 * R; ++h) {   // rows 4 h + cq
+                    const bool in = all || ((ok >> (h >> 1) & 1u) && key + 4 * h + cq < key_end);
+                    const __nv_bfloat16 *src = kl + off[h >> 1] + (h & 1 ? row4 : 0);
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const bool have = in && (FULL || 4 * i + t <= last_piece);
-                        cp16(dst + (r * (D / 32) + i) * 512, have ? kl + off[r] + 32 * i : p.k, have);
+                    for (int d = 0; d < DB; ++d) {
+                        const bool have = in && (FULL || 8 * d + cj <= last_piece);
+                        cp16(dst + k_to + (4 * h * DB + d) * 128, have ? src + 64 * d : p.k, have);
                     }
                 }
                 ++k_tile;
@@ -306,17 +318,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 const uint32_t ok = ok_bits >> (8 * (v_tile & 3)) & kAll;
                 const bool all = ok == kAll && key + KT <= key_end;
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int h = 0; h < 2 * R; ++h) {
+                    const bool in = all || ((ok >> (h >> 1) & 1u) && key + 4 * h + cq < key_end);
+                    const __nv_bfloat16 *src = vl + off[h >> 1] + (h & 1 ? row4 : 0);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const bool in = all || ((ok >> r & 1u) && key + 8 * r + 2 * t + e < key_end);
-                        const __nv_bfloat16 *src = vl + off[r] + e * p.row_stride;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            const bool have = in && (FULL || 8 * d + g <= last_piece);
-                            cp16(dst + ((2 * r + e) * DB + d) * 512, have ? src + 64 * d : p.v, have);
-                        }
+                    for (int d = 0; d < DB; ++d) {
+                        const bool have = in && (FULL || 8 * d + cj <= last_piece);
+                        cp16(dst + v_to + (h & 1 ? v_chunk1 : v_chunk0) + (4 * h * DB + d) * 128, have ? src + 64 * d : p.v, have);
                     }
+                }
                 ++v_tile;
                 slot = slot + 1 == ST ? 0 : slot + 1;
             }
@@ -371,7 +381,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         for (int tile = 0; tile < tiles; ++tile) {
             // S^T = K Q^T: rows g and g + 8 of row tile k are keys 16 k + g and 16 k + 8 + g, columns the
             // heads 2 t and 2 t + 1 of each tile of 8
+            // (the barrier also ends every lane's reads of the piece before, whose slot is filled next)
             cp_wait<ST - 2>();
+            __syncwarp();
             float s[NT][M][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -383,7 +395,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 for (int i = 0; i < D / 32; ++i)
 #pragma unroll
                     for (int k = 0; k < M; ++k) {
-                        uint4 a = lds16(src + (2 * k * (D / 32) + i) * 512), c = lds16(src + ((2 * k + 1) * (D / 32) + i) * 512);
+                        const uint32_t at = src + (k_from ^ (i & 1 ? 64u : 0u)) + (16 * k * DB + (i >> 1)) * 128;
+                        uint4 a = lds16(at), c = lds16(at + 8 * DB * 128);
                         if (!FULL && tail < 8 && 4 * i + t == last_piece) {   // what lies behind head_dim may be anything
                             const uint32_t k0 = tail >= 2 ? 0xffffffffu : 0xffffu, k1 = tail >= 4 ? 0xffffffffu : tail == 3 ? 0xffffu : 0u;
                             const uint32_t k2 = tail >= 6 ? 0xffffffffu : tail == 5 ? 0xffffu : 0u, k3 = tail == 7 ? 0xffffu : 0u;
@@ -476,14 +489,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
             // O^T += V^T P^T: of row tile k, lane (g, t) holds features 64 d + 8 g .. + 7 of keys
             // 16 k + 2t, 2t + 1, 2t + 8 and 2t + 9
             cp_wait<ST - 2>();
+            __syncwarp();
             {
-                const uint32_t src = ring + use * kPiece;
+                const uint32_t src = ring + use * kPiece + v_from;
 #pragma unroll
                 for (int k = 0; k < M; ++k)
 #pragma unroll
                     for (int d = 0; d < DB; ++d) {
-                        const uint4 v0 = lds16(src + ((4 * k) * DB + d) * 512), v1 = lds16(src + ((4 * k + 1) * DB + d) * 512);
-                        const uint4 v2 = lds16(src + ((4 * k + 2) * DB + d) * 512), v3 = lds16(src + ((4 * k + 3) * DB + d) * 512);
+                        const uint32_t at = src + (16 * k * DB + d) * 128;
+                        const uint4 v0 = lds16(at), v1 = lds16(at + DB * 128);
+                        const uint4 v2 = lds16(at + 8 * DB * 128), v3 = lds16(at + 9 * DB * 128);
                         const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
                         const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
