@@ -46,7 +46,7 @@ struct AttnParams {
     int page_shift;
     const int32_t *lens;
     int n_seqs, n_heads, group;       // group: query heads per key-value head
-    int vheads, vper, per_vhead;      // virtual key-value heads: vheads = kv heads x vper, each with up to per_vhead query heads
+    int n_kv, vheads, vper, per_vhead;   // virtual key-value heads: vheads = n_kv x vper, each with up to per_vhead query heads
     int head_dim;
     float scale_log2;                 // scale log2 e
     void *o;
@@ -56,6 +56,7 @@ struct AttnParams {
     float *part;                      // [grid, 2] partials
     uint32_t *status;
     int unit;                         // keys per unit
+    int shift;                        // rows of the ring have a chunk to spare, and pages hold whole sectors (see the kernel)
     int q_vec;                        // Q's rows and heads lie on 16 bytes
     int grid;                         // CTAs of the first launch (those behind the number of units stay idle)
 };
@@ -189,11 +190,35 @@ __host__ __device__ __forceinline__ int part_floats(int per_vhead, int head_dim)
     return (per_vhead * (part_row(head_dim) + 2) + 3) & ~3;
 }
 
-template <int NT>
+// shared memory behind the ring: the four warps' results of 8 heads x up to 128 features at a time
+template <int DB>
 struct AttnShared {
+    static constexpr int kFeatures = DB < 2 ? 64 : 128;
+    float o[kWarps][8][kFeatures];
+    float m[kWarps][8], l[kWarps][8];
     int64_t scan[2 * kWarps];
-    float m[kWarps][8 * NT], l[kWarps][8 * NT];   // every warp's maximum and sum of each query head
     int at;
+};
+
+// A place in the list of units: sequence b (len keys, n units per head), part `sub` of the query heads of
+// key-value head kv, unit j of it.
+struct Walker {
+    int b, len, n, kv, sub, j;
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        if (++j < n) return;
+        j = 0;
+        if (++sub < p.vper) return;
+        sub = 0;
+        if (++kv < p.n_kv) return;
+        kv = 0;
+        do {   // sequences without keys have no units
+            ++b;
+            len = b < p.n_seqs ? length_of(p, b) : 0;
+            n = (len + p.unit - 1) / p.unit;
+        } while (n == 0 && b < p.n_seqs);
+    }
+    __device__ __forceinline__ int head0(const AttnParams &p) const { return kv * p.group + sub * p.per_vhead; }
+    __device__ __forceinline__ int heads(const AttnParams &p) const { return min(p.per_vhead, p.group - sub * p.per_vhead); }
 };
 
 // DB: 64-feature blocks (head_dim <= 64 DB), NT: tiles of 8 query heads, KT: keys a warp takes at once (16 or 32),
@@ -209,8 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     // The ring comes first, on 128 bytes: a copy whose 32-byte sector straddles two of shared memory's is split, and
     // L2 then delivers the sector twice (measured: 671 MB for 336, 5.4 instead of 6.9 TB/s).
     extern __shared__ __align__(128) uint8_t smem[];
-    AttnShared<NT> &sh = *reinterpret_cast<AttnShared<NT> *>(smem + kWarps * ST * kPiece);
-    auto &s_m = sh.m, &s_l = sh.l;
+    AttnShared<DB> &sh = *reinterpret_cast<AttnShared<DB> *>(smem + kWarps * ST * kPiece);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -233,229 +257,240 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     const int64_t units = sum_units(p, 0, &first, sh.scan);
     const int ctas = static_cast<int>(units < p.grid ? units : p.grid);   // every one of them gets a unit
     if (static_cast<int>(blockIdx.x) >= ctas) return;
-    const int64_t lo = range_start(units, ctas, blockIdx.x), hi = range_start(units, ctas, blockIdx.x + 1);
-    int b = find_seq(p, lo, &first, sh.scan, &sh.at);
+    const int64_t lo = range_start(units, ctas, blockIdx.x);
+    const int todo = static_cast<int>(range_start(units, ctas, blockIdx.x + 1) - lo);
+    Walker at;   // the unit being worked on
+    at.b = find_seq(p, lo, &first, sh.scan, &sh.at);
+    at.len = length_of(p, at.b);
+    at.n = (at.len + kUnit - 1) / kUnit;
+    const int vhead = static_cast<int>((lo - first) / at.n);
+    at.kv = vhead / p.vper;
+    at.sub = vhead % p.vper;
+    at.j = static_cast<int>((lo - first) % at.n);
 
-    // The ring holds rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take a
-    // segment, 16 bytes each.  A 16-byte chunk j lies at j ^ 4 (r & 1) of its segment for K, j ^ (r & 6) for V, so
-    // that the eight lanes of a read phase (below) meet eight different chunks.
+    // A piece in the ring: rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take
+    // a segment, 16 bytes each.  The 16-byte chunk k of a segment lies at k ^ 4 (r & 1) for K, k ^ (r & 6) for V, so
+    // that the eight lanes of a read phase (below) meet eight different chunks.  Where rows may start in the middle of
+    // a 32-byte sector (p.shift: the ring's rows have a chunk to spare then), those rows lie one chunk further on, so
+    // that sectors stay whole; which ones depends on the head (`odd`) and, for strides of an odd number of chunks, on
+    // the row.
     const uint32_t ring = smem_u32(smem) + warp * (ST * kPiece);
     const int cq = lane >> 3, cj = lane & 7;   // copies: row of four, chunk
-    const uint32_t k_to = cq * DB * 128 + ((cj ^ (4 * (cq & 1))) << 4);
-    const uint32_t v_to = cq * DB * 128;       // + chunk, which depends on the row of eight
-    const uint32_t v_chunk0 = (cj ^ (cq & 2)) << 4, v_chunk1 = (cj ^ (4 + (cq & 2))) << 4;
-    const uint32_t k_from = g * DB * 128 + ((t ^ (4 * (g & 1))) << 4);   // chunk t; chunk 4 + t is at ^ 64
-    const uint32_t v_from = 2 * t * DB * 128 + ((g ^ (2 * t)) << 4);
-    // the 16-byte pieces of a row that hold features; the last one may hold fewer than 8
-    const int last_piece = (p.head_dim - 1) >> 3, tail = p.head_dim - 8 * last_piece;
+    const uint32_t turn = FULL ? 0u : static_cast<uint32_t>(p.shift) & static_cast<uint32_t>(p.row_stride >> 3);   // odd rows differ from even ones
+    auto odd_of = [&](const __nv_bfloat16 *head) { return FULL ? 0u : static_cast<uint32_t>(p.shift) & static_cast<uint32_t>(reinterpret_cast<uintptr_t>(head) >> 4); };
+    const int last_piece = (p.head_dim - 1) >> 3;   // the last 16-byte piece of a row that holds features
     const int row_mask = (1 << p.page_shift) - 1;
-    const int64_t row4 = 4 * p.row_stride;
-    bool have[DB];   // this lane's chunk of each segment holds features; zeros are stored for one that does not
+    const int64_t row4 = 4 * p.row_stride, lane_at = cq * p.row_stride + 8 * cj;
+    const bool one_page = ((KT - 1) >> p.page_shift) == 0;   // a tile lies in one page
+    bool have[DB];   // this lane's chunk of each segment holds features
 #pragma unroll
     for (int d = 0; d < DB; ++d) have[d] = FULL || 8 * d + cj <= last_piece;
+    // words of K's pieces 4 (last_piece / 4) + t that hold features: what lies behind head_dim may be anything
+    uint32_t keep[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int left = p.head_dim - 8 * ((last_piece & ~3) + t) - 2 * e;
+        keep[e] = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+    }
 
-    int64_t u = lo;
-    while (u < hi) {
-        const int len = length_of(p, b);
-        const int64_t n_units = (len + kUnit - 1) / kUnit;
-        if (u >= first + n_units * p.vheads) {   // behind this sequence
-            first += n_units * p.vheads;
-            ++b;
-            continue;
+    // ---- copies, ahead of the work: unit `ahead` is the next whose K goes into the ring
+    Walker ahead = at;
+    int copied = 0, slot = 0;          // units whose K and V have been begun, ring slot for the next piece
+    const int32_t *list = nullptr;     // ahead's page list
+    const __nv_bfloat16 *kh = nullptr, *vh = nullptr;   // its head's keys and values
+    int next[R];                       // pages of its groups of 8 keys (loaded one unit before their use)
+    int64_t off[R];                    // offset of each group's first row
+    uint32_t bits = 0;                 // 8 bits per unit in flight: a group's page is valid
+    bool plain = false;                // every row of the tile is there
+    auto enter = [&]() {
+        const int64_t head = ahead.kv * p.head_stride;
+        kh = p.k + head;
+        vh = p.v + head;
+        list = p.pages + ahead.b * p.max_pages;
+    };
+    auto look_up = [&]() {
+        const int key = ahead.j * kUnit + KT * warp;
+        next[0] = key < ahead.len ? __ldg(list + (key >> p.page_shift)) : -1;
+        if (!one_page) {
+#pragma unroll
+            for (int r = 1; r < R; ++r) next[r] = key + 8 * r < ahead.len ? __ldg(list + ((key + 8 * r) >> p.page_shift)) : -1;
         }
-        const int vh = static_cast<int>((u - first) / n_units);
-        const int64_t seg_first = first + vh * n_units, seg_end = seg_first + n_units;
-        const int64_t end = seg_end < hi ? seg_end : hi;
-        const int kvh = vh / p.vper, head0 = kvh * p.group + (vh % p.vper) * p.per_vhead;
-        const int heads = min(p.per_vhead, (kvh + 1) * p.group - head0);
-
-        // this warp's tiles: KT keys from key0, + kUnit, ...
-        const int key0 = static_cast<int>((u - seg_first) * kUnit) + KT * warp;
-        const int key_end = min(len, static_cast<int>((end - seg_first) * kUnit));
-        const int tiles = key_end > key0 ? (key_end - key0 + kUnit - 1) / kUnit : 0;
-        const int32_t *list = p.pages + b * p.max_pages;
-        const __nv_bfloat16 *kl = p.k + kvh * p.head_stride + cq * p.row_stride + 8 * cj;
-        const __nv_bfloat16 *vl = p.v + kvh * p.head_stride + cq * p.row_stride + 8 * cj;
-
-        // the pages of the next tile to be copied are loaded one tile ahead
-        int next[R];
-        auto look_up = [&](int key) {
-            next[0] = key < key_end ? __ldg(list + (key >> p.page_shift)) : -1;
-            if ((KT - 1) >> p.page_shift) {   // pages smaller than a tile
+    };
+    // copies one piece: rows 4 h + cq of the groups
+    auto copy = [&](const __nv_bfloat16 *head, bool values, int key, uint32_t ok) {
+        const __nv_bfloat16 *from = head + lane_at;
+        const uint32_t on = FULL ? 0u : (odd_of(head) ^ (cq & turn)) & 1u;
+        const uint32_t chunk = (cj + on) & 7, dst = ring + slot * kPiece + cq * DB * 128 + ((cj + on) >> 3) * 128;
+        const uint32_t to0 = dst + ((chunk ^ (values ? cq & 2 : 4 * (cq & 1))) << 4);
+        const uint32_t to1 = values ? to0 ^ 64u : to0;   // rows 4 to 7 of a group
+        if (plain) {   // the common case without a test per row
 #pragma unroll
-                for (int r = 1; r < R; ++r) next[r] = key + 8 * r < key_end ? __ldg(list + ((key + 8 * r) >> p.page_shift)) : -1;
-            } else {
+            for (int h = 0; h < 2 * R; ++h) {
+                const uint32_t to = (h & 1 ? to1 : to0) + 4 * h * DB * 128;
+                const __nv_bfloat16 *src = from + off[h >> 1] + (h & 1 ? row4 : 0);
 #pragma unroll
-                for (int r = 1; r < R; ++r) next[r] = next[0];
+                for (int d = 0; d < DB; ++d)
+                    if (FULL || have[d]) cp16(to + d * 128, src + 64 * d);
             }
-        };
-        int64_t off[R];         // of the tile last begun: offset of each group's first row
-        uint32_t ok_bits = 0;   // 8 bits per tile in flight: its groups' pages are valid
-        int k_tile = 0, v_tile = 0, slot = 0;   // next tile to be copied, ring slot for it
-        auto issue_k = [&]() {
-            if (k_tile < tiles) {
-                const int key = key0 + k_tile * kUnit;
-                const uint32_t dst = ring + slot * kPiece;
-                uint32_t ok = 0;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2 * R; ++h) {
+                const uint32_t to = (h & 1 ? to1 : to0) + 4 * h * DB * 128;
+                const __nv_bfloat16 *src = from + off[h >> 1] + (h & 1 ? row4 : 0);
+                const bool in = (ok >> (h >> 1) & 1u) && key + 4 * h + cq < ahead.len;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    if (FULL || have[d]) cp16_or_zero(to + d * 128, in ? src + 64 * d : p.k, in);
+            }
+        }
+    };
+    auto issue_k = [&]() {
+        if (copied < todo) {
+            const int key = ahead.j * kUnit + KT * warp;
+            uint32_t ok = 0;
+            if (one_page) {
+                const bool fine = next[0] >= 0 && next[0] < p.n_pages;
+                off[0] = fine ? next[0] * p.page_stride + (key & row_mask) * p.row_stride : 0;
+#pragma unroll
+                for (int r = 1; r < R; ++r) off[r] = off[r - 1] + 2 * row4;
+                ok = fine ? kAll : 0u;
+            } else {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const bool fine = next[r] >= 0 && next[r] < p.n_pages;
-                    ok |= fine ? 1u << r : 0u;
                     off[r] = fine ? next[r] * p.page_stride + ((key + 8 * r) & row_mask) * p.row_stride : 0;
+                    ok |= fine ? 1u << r : 0u;
                 }
-                const bool all = ok == kAll && key + KT <= key_end;
-                if (!all && lane == 0) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (key + 8 * r < key_end && !(ok >> r & 1u)) atomicOr(p.status, kStatusBadIndex);
-                }
-                ok_bits = (ok_bits & ~(0xffu << (8 * (k_tile & 3)))) | (ok << (8 * (k_tile & 3)));
-                look_up(key + kUnit);
-                if (all) {   // the common case without a test per row
-#pragma unroll
-                    for (int h = 0; h < 2 * R; ++h) {   // rows 4 h + cq
-                        const __nv_bfloat16 *src = kl + off[h >> 1] + (h & 1 ? row4 : 0);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            if (FULL) cp16(dst + k_to + (4 * h * DB + d) * 128, src + 64 * d);
-                            else cp16_or_zero(dst + k_to + (4 * h * DB + d) * 128, src + (have[d] ? 64 * d : 0), have[d]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2 * R; ++h) {
-                        const bool in = (ok >> (h >> 1) & 1u) && key + 4 * h + cq < key_end;
-                        const __nv_bfloat16 *src = in ? kl + off[h >> 1] + (h & 1 ? row4 : 0) : p.k;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            cp16_or_zero(dst + k_to + (4 * h * DB + d) * 128, src + (have[d] ? 64 * d : 0), in && have[d]);
-                    }
-                }
-                ++k_tile;
-                slot = slot + 1 == ST ? 0 : slot + 1;
             }
-            cp_commit();
-        };
-        auto issue_v = [&]() {
-            if (v_tile < tiles) {
-                const int key = key0 + v_tile * kUnit;
-                const uint32_t dst = ring + slot * kPiece;
-                const uint32_t ok = ok_bits >> (8 * (v_tile & 3)) & kAll;
-                const bool all = ok == kAll && key + KT <= key_end;
-                if (all) {   // the common case without a test per row
+            plain = ok == kAll && key + KT <= ahead.len;
+            if (!plain && lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < 2 * R; ++h) {   // rows 4 h + cq
-                        const __nv_bfloat16 *src = vl + off[h >> 1] + (h & 1 ? row4 : 0);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            if (FULL) cp16(dst + v_to + (h & 1 ? v_chunk1 : v_chunk0) + (4 * h * DB + d) * 128, src + 64 * d);
-                            else cp16_or_zero(dst + v_to + (h & 1 ? v_chunk1 : v_chunk0) + (4 * h * DB + d) * 128, src + (have[d] ? 64 * d : 0), have[d]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2 * R; ++h) {
-                        const bool in = (ok >> (h >> 1) & 1u) && key + 4 * h + cq < key_end;
-                        const __nv_bfloat16 *src = in ? vl + off[h >> 1] + (h & 1 ? row4 : 0) : p.v;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            cp16_or_zero(dst + v_to + (h & 1 ? v_chunk1 : v_chunk0) + (4 * h * DB + d) * 128, src + (have[d] ? 64 * d : 0), in && have[d]);
-                    }
-                }
-                ++v_tile;
-                slot = slot + 1 == ST ? 0 : slot + 1;
+                for (int r = 0; r < R; ++r)
+                    if (!(ok >> r & 1u) && key + 8 * r < ahead.len) atomicOr(p.status, kStatusBadIndex);
             }
-            cp_commit();
-        };
-        look_up(key0);
-        issue_k();
-        issue_v();
-        if (ST == 4) issue_k();
+            bits = (bits & ~(0xffu << (8 * (copied & 3)))) | ok << (8 * (copied & 3));
+            if (key < ahead.len) copy(kh, false, key, ok);
+            slot = slot + 1 == ST ? 0 : slot + 1;
+        }
+        cp_commit();
+    };
+    auto issue_v = [&]() {
+        if (copied < todo) {
+            const int key = ahead.j * kUnit + KT * warp;
+            if (key < ahead.len) copy(vh, true, key, bits >> (8 * (copied & 3)));
+            slot = slot + 1 == ST ? 0 : slot + 1;
+            if (++copied < todo) {
+                ahead.next(p);
+                if (ahead.j == 0) enter();
+                look_up();
+            }
+        }
+        cp_commit();
+    };
 
-        // Q fragments: column g of tile n is query head head0 + 8 n + g; piece i of lane (g, t) is
-        // features 32 i + 8 t .. + 7, the same that the lane holds of a key
-        uint4 qf[NT][D / 32];
+    // Q fragments: column g of tile n is query head 8 n + g of the virtual head; piece i of lane (g, t) is
+    // features 32 i + 8 t .. + 7, the same that the lane holds of a key
+    uint4 qf[NT][D / 32];
+    auto load_q = [&](const Walker &w) {
+        const int head0 = w.head0(p), heads = w.heads(p);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const int h = 8 * n + g, f = 32 * i + 8 * t;
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + b * p.ldq +
+                uint32_t x[4] = {0u, 0u, 0u, 0u};
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + w.b * p.ldq +
                                       static_cast<int64_t>(head0 + h) * p.head_dim + f;
                 if (h < heads) {
                     if (p.q_vec) {
                         if (FULL || f < p.head_dim) {
-                            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
-                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
+                            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (f + e < p.head_dim) w[e >> 1] |= static_cast<uint32_t>(__ldg(src + e)) << (16 * (e & 1));
+                            if (f + e < p.head_dim) x[e >> 1] |= static_cast<uint32_t>(__ldg(src + e)) << (16 * (e & 1));
                     }
                 }
-                qf[n][i] = make_uint4(w[0], w[1], w[2], w[3]);
+                qf[n][i] = make_uint4(x[0], x[1], x[2], x[3]);
             }
+    };
 
-        float o[NT][DB][4][4];
-        float m[NT][2], l[NT][2];
+    enter();
+    look_up();
+    load_q(at);
+    issue_k();
+    issue_v();
+    if (ST == 4) issue_k();
+
+    float o[NT][DB][4][4];
+    float m[NT][2], l[NT][2];
+    int use = 0, seg_from = 0;   // ring slot of the next piece to be used; unit that began this head
+    for (int done = 0; done < todo; ++done) {
+        if (done == seg_from) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.0f;
+            for (int n = 0; n < NT; ++n) {
+                m[n][0] = m[n][1] = -INFINITY;
+                l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+                for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
+                    for (int w = 0; w < 4; ++w)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[n][d][w][c] = 0.0f;
+                        for (int c = 0; c < 4; ++c) o[n][d][w][c] = 0.0f;
+            }
         }
+        const int key = at.j * kUnit + KT * warp;
+        const uint32_t now = bits >> (8 * (done & 3));
+        const bool live = key < at.len;   // the same for the whole warp
 
-        int use = 0;   // ring slot of the next piece to be used
-        for (int tile = 0; tile < tiles; ++tile) {
-            // S^T = K Q^T: rows g and g + 8 of row tile k are keys 16 k + g and 16 k + 8 + g, columns the
-            // heads 2 t and 2 t + 1 of each tile of 8
-            // (the barrier also ends every lane's reads of the piece before, whose slot is filled next)
-            cp_wait<ST - 2>();
-            __syncwarp();
-            float s[NT][M][4];
+        // S^T = K Q^T: rows g and g + 8 of row tile k are keys 16 k + g and 16 k + 8 + g, columns the heads 2 t
+        // and 2 t + 1 of each tile of 8.  (The barrier also ends every lane's reads of the piece before, whose slot
+        // is filled next.)
+        cp_wait<ST - 2>();
+        __syncwarp();
+        float s[NT][M][4];
+        if (live) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int k = 0; k < M; ++k) s[n][k][0] = s[n][k][1] = s[n][k][2] = s[n][k][3] = 0.0f;
-            {
-                const uint32_t src = ring + use * kPiece;
+            // places of pieces t (even i) and 4 + t (odd i) in row g
+            const uint32_t on = FULL ? 0u : (odd_of(p.k + at.kv * p.head_stride) ^ (g & turn)) & 1u;
+            const uint32_t src = ring + use * kPiece + g * DB * 128, swz = 4 * (g & 1);
+            const uint32_t even = src + (((t + on) ^ swz) << 4);
+            const uint32_t odd = src + ((4 + t + on) >> 3) * 128 + ((((4 + t + on) & 7) ^ swz) << 4);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+            for (int k = 0; k < M; ++k) {
 #pragma unroll
-                    for (int k = 0; k < M; ++k) {
-                        const uint32_t at = src + (k_from ^ (i & 1 ? 64u : 0u)) + (16 * k * DB + (i >> 1)) * 128;
-                        uint4 a = lds16(at), c = lds16(at + 8 * DB * 128);
-                        if (!FULL && tail < 8 && 4 * i + t == last_piece) {   // what lies behind head_dim may be anything
-                            const uint32_t k0 = tail >= 2 ? 0xffffffffu : 0xffffu, k1 = tail >= 4 ? 0xffffffffu : tail == 3 ? 0xffffu : 0u;
-                            const uint32_t k2 = tail >= 6 ? 0xffffffffu : tail == 5 ? 0xffffu : 0u, k3 = tail == 7 ? 0xffffu : 0u;
-                            a = make_uint4(a.x & k0, a.y & k1, a.z & k2, a.w & k3);
-                            c = make_uint4(c.x & k0, c.y & k1, c.z & k2, c.w & k3);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma(s[n][k], a.x, c.x, a.y, c.y, qf[n][i].x, qf[n][i].y);
-                            mma(s[n][k], a.z, c.z, a.w, c.w, qf[n][i].z, qf[n][i].w);
-                        }
+                for (int i = 0; i < D / 32; ++i) {
+                    if (!FULL && 4 * i > last_piece) break;
+                    const uint32_t piece = (i & 1 ? odd : even) + (16 * k * DB + (i >> 1)) * 128;
+                    uint4 a = lds16(piece), c = lds16(piece + 8 * DB * 128);
+                    if (!FULL && 4 * i + 3 >= last_piece) {
+                        a = make_uint4(a.x & keep[0], a.y & keep[1], a.z & keep[2], a.w & keep[3]);
+                        c = make_uint4(c.x & keep[0], c.y & keep[1], c.z & keep[2], c.w & keep[3]);
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma(s[n][k], a.x, c.x, a.y, c.y, qf[n][i].x, qf[n][i].y);
+                        mma(s[n][k], a.z, c.z, a.w, c.w, qf[n][i].z, qf[n][i].w);
+                    }
+                }
             }
-            use = use + 1 == ST ? 0 : use + 1;
-            if (ST == 4) issue_v(); else issue_k();
+        }
+        use = use + 1 == ST ? 0 : use + 1;
+        if (ST == 4) issue_v(); else issue_k();
 
-            // mask, running maximum, p
-            const int key = key0 + tile * kUnit;
-            const uint32_t ok = ok_bits >> (8 * (tile & 3)) & kAll;
-            if (ok != kAll || key + KT > key_end) {
+        // mask, running maximum, p
+        uint32_t ph[NT][M][2], pl[NT][M][2];
+        if (live) {
+            if ((now & kAll) != kAll || key + KT > at.len) {
 #pragma unroll
                 for (int k = 0; k < M; ++k) {
-                    const bool in0 = (ok >> (2 * k) & 1u) && key + 16 * k + g < key_end;
-                    const bool in1 = (ok >> (2 * k + 1) & 1u) && key + 16 * k + 8 + g < key_end;
+                    const bool in0 = (now >> (2 * k) & 1u) && key + 16 * k + g < at.len;
+                    const bool in1 = (now >> (2 * k + 1) & 1u) && key + 16 * k + 8 + g < at.len;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -469,7 +504,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
 #pragma unroll
                         for (int c = 0; c < 4; ++c) s[n][k][c] *= p.scale_log2;
             }
-            uint32_t ph[NT][M][2], pl[NT][M][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float x0 = fmaxf(s[n][0][0], s[n][0][2]), x1 = fmaxf(s[n][0][1], s[n][0][3]);
@@ -520,43 +554,63 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                         pl[n][k][r] = transpose8x8(pl[n][k][r]);
                     }
             }
+        }
 
-            // O^T += V^T P^T: of row tile k, lane (g, t) holds features 64 d + 8 g .. + 7 of keys
-            // 16 k + 2t, 2t + 1, 2t + 8 and 2t + 9
-            cp_wait<ST - 2>();
-            __syncwarp();
-            {
-                const uint32_t src = ring + use * kPiece + v_from;
+        // O^T += V^T P^T: of row tile k, lane (g, t) holds features 64 d + 8 g .. + 7 of keys 16 k + 2t, 2t + 1,
+        // 2t + 8 and 2t + 9
+        cp_wait<ST - 2>();
+        __syncwarp();
+        if (live) {
+            // places of piece g in rows 2 t and 2 t + 1
+            const uint32_t on = odd_of(p.v + at.kv * p.head_stride) & 1u, c0 = g + on, c1 = g + (on ^ (turn & 1u));
+            const uint32_t src = ring + use * kPiece + 2 * t * DB * 128;
+            const uint32_t row0 = src + (c0 >> 3) * 128 + (((c0 & 7) ^ (2 * t)) << 4);
+            const uint32_t row1 = src + DB * 128 + (c1 >> 3) * 128 + (((c1 & 7) ^ (2 * t)) << 4);
 #pragma unroll
-                for (int k = 0; k < M; ++k)
+            for (int k = 0; k < M; ++k) {
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const uint32_t at = src + (16 * k * DB + d) * 128;
-                        const uint4 v0 = lds16(at), v1 = lds16(at + DB * 128);
-                        const uint4 v2 = lds16(at + 8 * DB * 128), v3 = lds16(at + 9 * DB * 128);
-                        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-                        const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+                for (int d = 0; d < DB; ++d) {
+                    if (!FULL && 8 * d > last_piece) break;
+                    const uint32_t step = (16 * k * DB + d) * 128;
+                    const uint4 v0 = lds16(row0 + step), v1 = lds16(row1 + step);
+                    const uint4 v2 = lds16(row0 + step + 8 * DB * 128), v3 = lds16(row1 + step + 8 * DB * 128);
+                    const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                    const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
-                            const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
-                            const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+                    for (int w = 0; w < 4; ++w) {
+                        // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
+                        const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
+                        const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                mma(o[n][d][w], a0, a1, a2, a3, ph[n][k][0], ph[n][k][1]);
-                                mma(o[n][d][w], a0, a1, a2, a3, pl[n][k][0], pl[n][k][1]);
-                            }
+                        for (int n = 0; n < NT; ++n) {
+                            mma(o[n][d][w], a0, a1, a2, a3, ph[n][k][0], ph[n][k][1]);
+                            mma(o[n][d][w], a0, a1, a2, a3, pl[n][k][0], pl[n][k][1]);
                         }
                     }
+                }
             }
-            use = use + 1 == ST ? 0 : use + 1;
-            if (ST == 4) issue_k(); else issue_v();
         }
-        cp_wait<0>();
+        use = use + 1 == ST ? 0 : use + 1;
+        if (ST == 4) issue_k(); else issue_v();
 
-        // join the four warps through shared memory (the ring is empty now)
-        float *s_o = reinterpret_cast<float *>(smem);   // [warp][head][D]
-        __syncthreads();
+        const bool ends = at.j + 1 == at.n;
+        if (!ends && done + 1 < todo) {
+            ++at.j;
+            continue;
+        }
+        // The head ends here, or this CTA's range does: join the four warps through shared memory, while the copies
+        // for the next head are on their way.
+        const int head0 = at.head0(p), heads = at.heads(p);
+        const bool whole = ends && at.j == done - seg_from;
+        const int b = at.b;
+        float *part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_from == 0 ? 0 : 1)) * part_floats(p.per_vhead, p.head_dim);
+        const int row = part_row(p.head_dim);
+        if (done + 1 < todo) {
+            at.next(p);
+            load_q(at);
+        }
+        seg_from = done + 1;
+        constexpr int kF = AttnShared<DB>::kFeatures;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -564,60 +618,62 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], w);
                 l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], w);
             }
+            const int mine = min(8, heads - 8 * n);   // heads of this tile
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int h = 8 * n + 2 * t + c;
-                if (h >= heads) continue;
-                if (g == 0) {
-                    s_m[warp][h] = m[n][c];
-                    s_l[warp][h] = l[n][c];
+            for (int f0 = 0; f0 < D; f0 += kF) {
+                __syncthreads();   // the buffer is free
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 2 * t + c;
+                    if (h >= mine) continue;
+                    if (g == 0) {
+                        sh.m[warp][h] = m[n][c];
+                        sh.l[warp][h] = l[n][c];
+                    }
+#pragma unroll
+                    for (int d = f0 / 64; d < (f0 + kF) / 64; ++d) {
+                        float4 *dst = reinterpret_cast<float4 *>(&sh.o[warp][h][64 * d - f0 + 8 * g]);
+                        dst[0] = make_float4(o[n][d][0][c], o[n][d][0][2 + c], o[n][d][1][c], o[n][d][1][2 + c]);
+                        dst[1] = make_float4(o[n][d][2][c], o[n][d][2][2 + c], o[n][d][3][c], o[n][d][3][2 + c]);
+                    }
                 }
+                __syncthreads();
+                for (int i = threadIdx.x; i < mine * kF; i += kWarps * 32) {
+                    const int h = i / kF, d = f0 + i % kF;
+                    float top = sh.m[0][h];
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    float4 *dst = reinterpret_cast<float4 *>(s_o + (warp * 8 * NT + h) * D + 64 * d + 8 * g);
-                    dst[0] = make_float4(o[n][d][0][c], o[n][d][0][2 + c], o[n][d][1][c], o[n][d][1][2 + c]);
-                    dst[1] = make_float4(o[n][d][2][c], o[n][d][2][2 + c], o[n][d][3][c], o[n][d][3][2 + c]);
+                    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.m[w][h]);
+                    const float z = top == -INFINITY ? 0.0f : top;
+                    float sum = 0.0f, x = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = exp2_fast(sh.m[w][h] - z);
+                        sum += f * sh.l[w][h];
+                        x += f * sh.o[w][h][i % kF];
+                    }
+                    const int64_t head = head0 + 8 * n + h;
+                    if (d < p.head_dim) {
+                        if (!whole) {
+                            part[(8 * n + h) * row + d] = x;
+                        } else {
+                            x *= sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+                            if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(x);
+                            else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = x;
+                        }
+                    }
+                    if (d == 0) {
+                        if (!whole) {
+                            part[p.per_vhead * row + 2 * (8 * n + h)] = top;
+                            part[p.per_vhead * row + 2 * (8 * n + h) + 1] = sum;
+                        } else if (p.lse) {
+                            p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
+                        }
+                    }
                 }
             }
         }
-        __syncthreads();
-        const bool whole = u == seg_first && end == seg_end;
-        float *part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (u == lo ? 0 : 1)) * part_floats(p.per_vhead, p.head_dim);
-        const int row = part_row(p.head_dim);
-        for (int h = warp; h < heads; h += kWarps) {
-            float top = s_m[0][h];
-#pragma unroll
-            for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][h]);
-            const float z = top == -INFINITY ? 0.0f : top;
-            float f[kWarps], sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                f[i] = exp2_fast(s_m[i][h] - z);
-                sum += f[i] * s_l[i][h];
-            }
-            const float inv = whole ? (sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum)) : 1.0f;
-            const int64_t head = head0 + h;
-            for (int d = lane; d < p.head_dim; d += 32) {
-                float x = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) x += f[i] * s_o[(i * 8 * NT + h) * D + d];
-                x *= inv;
-                if (!whole) part[h * row + d] = x;
-                else if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(x);
-                else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = x;
-            }
-            if (lane == 0) {
-                if (!whole) {
-                    part[p.per_vhead * row + 2 * h] = top;
-                    part[p.per_vhead * row + 2 * h + 1] = sum;
-                } else if (p.lse) {
-                    p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
-                }
-            }
-        }
-        __syncthreads();   // the ring is free again
-        u = end;
     }
+    cp_wait<0>();
 }
 
 // Joins the partials of the heads that more than one CTA of the first launch worked on: CTA (query head, sequence).
@@ -724,8 +780,9 @@ int per_vhead_of(int64_t group, int64_t head_dim) {
 
 template <int DB, int NT, int KT, int ST, bool FULL>
 cudaError_t go(AttnParams p, cudaStream_t s) {
-    constexpr int smem = kWarps * ST * KT * 64 * DB * 2 + static_cast<int>(sizeof(AttnShared<NT>));
-    static_assert(ST * KT * 2 >= 8 * NT * 4 && smem <= 227 * 1024, "the ring holds the join of the warps");
+    constexpr int smem = kWarps * ST * KT * 64 * DB * 2 + static_cast<int>(sizeof(AttnShared<DB>));
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+    p.shift = !FULL && (p.head_dim + 7) / 8 < 8 * DB && p.page_stride % 16 == 0 ? 1 : 0;
     const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, KT, ST, FULL>);
     cudaError_t e = smem_attr(f, smem);
     if (e != cudaSuccess) return e;
@@ -789,7 +846,8 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
     p.group = static_cast<int>(n_heads / c.n_kv_heads);
     p.per_vhead = per_vhead_of(p.group, c.head_dim);
     p.vper = (p.group + p.per_vhead - 1) / p.per_vhead;
-    p.vheads = c.n_kv_heads * p.vper;
+    p.n_kv = c.n_kv_heads;
+    p.vheads = p.n_kv * p.vper;
     p.head_dim = c.head_dim;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o = O; p.o_bf16 = o_bf16 ? 1 : 0; p.ldo = ldo; p.lse = lse;
