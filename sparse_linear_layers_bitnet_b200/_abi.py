@@ -203,12 +203,15 @@ def _launch(name: str, like, stream, *args) -> None:
     """Calls the entry point `name` with args and the stream, on the device of the
     tensor `like`: the current stream of that device unless one is given."""
     torch = _torch()
-    index = like.device.index
+    index = like.get_device()
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _launch(name, like, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    check(getattr(load(), name)(*args, s.cuda_stream), name)
+    # the current stream's handle, without the Stream object that torch.cuda.current_stream() makes (5 us a call)
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    status = getattr(load(), name)(*args, raw)
+    if status != BITNET_OK:
+        check(status, name)
 
 
 def _new(shape, dtype, like, stream):
@@ -221,14 +224,13 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _ws(ws, nbytes, like, stream):
-    """(tensor that holds it, address, size) of the workspace ws, or of one for this call
-    (whose status word nobody reads)."""
+def _ws(ws, size, like, stream):
+    """(tensor that holds it, address, bytes) of the workspace ws, or of one for this call
+    (whose status word nobody reads) of size() bytes."""
     if ws is not None:
-        assert ws.buf.device == like.device
+        assert ws.buf.get_device() == like.get_device()
         return ws.buf, ws.buf.data_ptr(), ws.nbytes
-    torch = _torch()
-    buf = _new((int(max(nbytes, 256)),), torch.uint8, like, stream)
+    buf = _new((max(size(), 256),), _torch().uint8, like, stream)
     return buf, buf.data_ptr(), buf.numel()
 
 
@@ -245,7 +247,7 @@ def _is(t, dtype, shape, like, optional=False) -> bool:
     """t is a contiguous tensor of that type and shape on like's device (or None, where optional)."""
     if t is None:
         return optional
-    return t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == like.device
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == like.get_device()
 
 
 def _dtype_code(dt) -> int:
@@ -527,7 +529,6 @@ def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumula
     (fp32 or bf16) of the normalised values; dR: the residual stream's own gradient, added to dH.
     Returns (dH, dw): dH of dR's (or dH's own) type, bf16 unless given; dw fp32."""
     torch = _torch()
-    lib = load()
     T, K = H.shape
     assert _is(H, torch.bfloat16, (T, K), H) and H.is_cuda and _is(rinv, torch.float32, (T,), H)
     assert dY.dtype in (torch.float32, torch.bfloat16) and _is(dY, dY.dtype, (T, K), H)
@@ -536,7 +537,7 @@ def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumula
     dH = _new((T, K), g, H, stream) if dH is None else dH
     dw = _new((K,), torch.float32, H, stream) if dw is None else dw
     assert _is(dR, g, (T, K), H, optional=True) and _is(dH, g, (T, K), H) and _is(dw, torch.float32, (K,), H)
-    keep, ws_ptr, ws_bytes = _ws(ws, lib.bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
+    keep, ws_ptr, ws_bytes = _ws(ws, lambda: load().bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
     _launch("bitnet_rmsnorm_grad", H, stream, dY.data_ptr(), _dtype_code(dY.dtype), H.data_ptr(), _addr(w),
             rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
             ws_ptr, ws_bytes)
@@ -586,14 +587,18 @@ def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, devic
 
 
 def _cache_struct(K, V) -> BitnetKvCache:
-    torch = _torch()
-    assert K.dim() == 4 and K.dtype == V.dtype == torch.bfloat16 and K.is_cuda and K.device == V.device
     n_pages, kv, page, d = K.shape
-    assert V.shape == K.shape and (d == 1 or K.stride(3) == V.stride(3) == 1)
-    # the stride of an axis of one says nothing: any valid one
-    (sp, sh, sr), other = ([st if n > 1 else -(-d // 8) * 8 for n, st in zip(t.shape[:3], t.stride())] for t in (K, V))
-    assert [sp, sh, sr] == other
-    return BitnetKvCache(K.data_ptr(), V.data_ptr(), n_pages, sp, sh, sr, page, kv, d)
+    strides = K.stride()
+    assert K.dtype is V.dtype is _torch().bfloat16 and K.is_cuda and K.get_device() == V.get_device() and V.shape == K.shape
+    if n_pages == 1 or kv == 1 or d == 1:
+        # the stride of an axis of one says nothing: any valid one
+        strides, other = ([st if n > 1 else -(-d // 8) * 8 for n, st in zip(t.shape[:3], t.stride())] + [t.stride(3) if d > 1 else 1]
+                          for t in (K, V))
+        assert strides == other
+    else:
+        assert V.stride() == strides
+    assert strides[3] == 1
+    return BitnetKvCache(K.data_ptr(), V.data_ptr(), n_pages, strides[0], strides[1], strides[2], page, kv, d)
 
 
 def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interleaved: bool = False,
@@ -612,9 +617,9 @@ def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interl
     assert two == 2 and _is(table, torch.float32, (n_pos, half, 2), X)
     if Y is None:
         Y = _new((T, n_heads * head_dim), X.dtype, X, stream)
-    assert Y.dim() == 2 and Y.dtype == X.dtype and Y.device == X.device and Y.stride(1) == 1
+    assert Y.dim() == 2 and Y.dtype == X.dtype and Y.get_device() == X.get_device() and Y.stride(1) == 1
     assert Y.shape[0] == T and Y.shape[1] >= n_heads * head_dim
-    keep, ws_ptr, ws_bytes = _ws(ws, 256, X, stream)
+    keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, X, stream)
     _launch("bitnet_rope", X, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(), table.data_ptr(), n_pos,
             T, n_heads, head_dim, 2 * half, 1 if interleaved else 0, 1 if inverse else 0, Y.data_ptr(), _ld(Y), ws_ptr,
             ws_bytes)
@@ -629,7 +634,7 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
     pages (int32 [sequences, most pages]).  table None: no rotation.  Returns Q (bf16 [T, heads * head_dim])."""
     torch = _torch()
     c = _cache_struct(K, V)
-    assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1 and QKV.device == K.device
+    assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1 and QKV.get_device() == K.get_device()
     T, width = QKV.shape
     heads = width // c.head_dim - 2 * c.n_kv_heads
     assert heads > 0 and width == (heads + 2 * c.n_kv_heads) * c.head_dim
@@ -640,7 +645,7 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
     assert _is(table, torch.float32, (n_pos, half, 2), QKV, optional=True)
     Q = _new((T, heads * c.head_dim), torch.bfloat16, QKV, stream) if Q is None else Q
     assert _is(Q, torch.bfloat16, (T, heads * c.head_dim), QKV)
-    keep, ws_ptr, ws_bytes = _ws(ws, 256, QKV, stream)
+    keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, QKV, stream)
     _launch("bitnet_rope_append", QKV, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV), pos.data_ptr(), _addr(seq),
             _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0, ctypes.byref(c), pages.data_ptr(), n_seqs,
             max_pages, Q.data_ptr(), ws_ptr, ws_bytes)
@@ -654,18 +659,18 @@ def bitnet_paged_attn(Q, K, V, pages, lens, scale: float | None = None, O=None, 
     bitnet_rope_append).  scale: head_dim^-1/2 unless given.  lse: fp32 [sequences, heads], filled when given.
     Returns O (bf16 unless o_dtype says fp32)."""
     torch = _torch()
-    lib = load()
     c = _cache_struct(K, V)
-    assert Q.dim() == 2 and Q.dtype == torch.bfloat16 and Q.stride(1) == 1 and Q.device == K.device
+    assert Q.dim() == 2 and Q.dtype == torch.bfloat16 and Q.stride(1) == 1 and Q.get_device() == K.get_device()
     n_seqs, width = Q.shape
     heads = width // c.head_dim
     assert heads > 0 and width == heads * c.head_dim
     assert pages.dim() == 2 and _is(pages, torch.int32, (n_seqs, pages.shape[1]), Q) and _is(lens, torch.int32, (n_seqs,), Q)
     if O is None:
         O = _new((n_seqs, width), torch.bfloat16 if o_dtype is None else o_dtype, Q, stream)
-    assert O.shape == Q.shape and O.stride(1) == 1 and O.device == Q.device and (o_dtype is None or O.dtype == o_dtype)
+    assert O.shape == Q.shape and O.stride(1) == 1 and O.get_device() == Q.get_device() and (o_dtype is None or O.dtype == o_dtype)
     assert _is(lse, torch.float32, (n_seqs, heads), Q, optional=True)
-    keep, ws_ptr, ws_bytes = _ws(ws, lib.bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream)
+    keep, ws_ptr, ws_bytes = _ws(
+        ws, lambda: load().bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream)
     _launch("bitnet_paged_attn", Q, stream, Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(),
             pages.shape[1], lens.data_ptr(), c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(),
             _dtype_code(O.dtype), _ld(O), _addr(lse), ws_ptr, ws_bytes)
