@@ -8,8 +8,9 @@
 // backward pass: the rotation is orthogonal) takes -s.
 //
 // Memory-bound: every head is read once and written once.  A thread owns one
-// place of the head (two vectors of VEC features that hold VEC pairs) and walks
-// over heads, so it reads its (c, s) once per token and keeps them in registers.
+// place of the head (the vectors of up to 16 bytes that hold its pairs) in
+// several heads of a row, so it reads its (c, s) once per row, and has all its
+// loads in flight before it looks at the row's position and page.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -43,6 +44,7 @@ struct RopeParams {
     int heads;                // heads per row that are rotated and go to y
     int kv_heads;             // append: key heads, then value heads behind them
     int head_dim, rot, inverse;
+    int table_vec;            // table rows lie on 16 bytes
     int places;               // threads per head
     int slots;                // heads a CTA holds at once
     // append
@@ -55,23 +57,83 @@ struct RopeParams {
     uint32_t *status;
 };
 
-constexpr int kRopeHeads = 4;   // heads a thread has in flight
+// vectors of a head that one thread holds: both halves of its pairs, or (interleaved) one vector of whole pairs
+template <int VEC, bool INTERLEAVED>
+constexpr int kVectors = INTERLEAVED && VEC > 1 ? 1 : 2;
+// heads per thread: 128 bytes of a row in flight, at most 8
+template <typename TI, int VEC, bool INTERLEAVED>
+constexpr int kHeads = 128 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) < 8
+                           ? 128 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) : 8;
 
 template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
+    constexpr int NV = kVectors<VEC, INTERLEAVED>, HEADS = kHeads<TI, VEC, INTERLEAVED>;
+    constexpr int PAIRS = NV * VEC / 2;
+    using VI = Vec<TI, VEC>;
+    using VO = Vec<TO, VEC>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t t = blockIdx.x;
     const int place = threadIdx.x % p.places, slot = threadIdx.x / p.places;
     if (slot >= p.slots) return;
+    // this place's vectors: pairs below `turned`, copied features behind them
+    const int half = p.rot >> 1;
+    const int turned = half / PAIRS;   // places that rotate
+    const bool turns = place < turned;
+    int off[2];
+    if (turns) {
+        off[0] = INTERLEAVED ? NV * VEC * place : VEC * place;
+        off[1] = INTERLEAVED ? off[0] + VEC : half + off[0];
+    } else {
+        off[0] = p.rot + NV * VEC * (place - turned);
+        off[1] = off[0] + VEC;
+    }
+    const bool has1 = NV == 2 && off[1] < p.head_dim;   // an odd count of copied vectors leaves the last one alone
+
+    // the heads' features first: they wait for nothing else
+    const int all = p.heads + 2 * p.kv_heads;
+    const int h0 = blockIdx.y * p.slots * HEADS + slot;
+    const TI *x = static_cast<const TI *>(p.x) + t * p.ldx;
+    VI v[HEADS][NV];
+#pragma unroll
+    for (int j = 0; j < HEADS; ++j) {
+        const int h = h0 + j * p.slots;
+        if (h < all) {
+            const TI *src = x + static_cast<int64_t>(h) * p.head_dim;
+            v[j][0] = *reinterpret_cast<const VI *>(src + off[0]);
+            if (has1) v[j][NV - 1] = *reinterpret_cast<const VI *>(src + off[1]);
+        }
+    }
+
     // the row's position, and for the cache its sequence, page and row in the page
     const int pos = __ldg(p.pos + t);
-    if (pos < 0) return;   // a padding row
+    int64_t seq = t;
+    if (APPEND && p.seq) seq = __ldg(p.seq + t);
+    if (pos < 0 || (APPEND && seq < 0)) return;   // a padding row
     int64_t cache_row = 0;
     bool bad = p.rot > 0 && pos >= p.n_pos;
+    float c[PAIRS], s[PAIRS];
+    if (turns && !bad) {
+        const float2 *row = p.table + static_cast<int64_t>(pos) * half + PAIRS * place;
+        if (PAIRS % 2 == 0 && p.table_vec) {
+#pragma unroll
+            for (int i = 0; i < PAIRS / 2; ++i) {
+                const float4 cs = __ldg(reinterpret_cast<const float4 *>(row) + i);
+                c[(2 * i) % PAIRS] = cs.x;
+                s[(2 * i) % PAIRS] = cs.y;
+                c[(2 * i + 1) % PAIRS] = cs.z;
+                s[(2 * i + 1) % PAIRS] = cs.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const float2 cs = __ldg(row + i);
+                c[i] = cs.x;
+                s[i] = cs.y;
+            }
+        }
+    }
     if (APPEND) {
-        const int64_t seq = p.seq ? static_cast<int64_t>(__ldg(p.seq + t)) : t;
-        if (seq < 0) return;   // a padding row
         const int64_t in_table = pos >> p.page_shift;
         bad = bad || seq >= p.n_seqs || in_table >= p.max_pages;
         if (!bad) {
@@ -84,89 +146,39 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
         return;
     }
-    // this place's two vectors: pairs below `turned`, copied features behind them
-    const int half = p.rot >> 1;
-    const int turned = half / VEC;   // places that rotate
-    const bool turns = place < turned;
-    int off_a, off_b;
-    bool has_b = true;
-    if (turns) {
-        off_a = INTERLEAVED ? 2 * VEC * place : VEC * place;
-        off_b = INTERLEAVED ? off_a + VEC : half + off_a;
-    } else {
-        off_a = p.rot + 2 * VEC * (place - turned);
-        off_b = off_a + VEC;
-        has_b = off_b < p.head_dim;
-    }
-    float c[VEC], s[VEC];
-    if (turns) {
-        const float2 *row = p.table + static_cast<int64_t>(pos) * half + VEC * place;
+    if (p.inverse) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float2 cs = __ldg(row + i);
-            c[i] = cs.x;
-            s[i] = p.inverse ? -cs.y : cs.y;
-        }
+        for (int i = 0; i < PAIRS; ++i) s[i] = -s[i];
     }
-    const TI *x = static_cast<const TI *>(p.x) + t * p.ldx;
     TO *y = static_cast<TO *>(p.y) + t * p.ldy;
-    const int all = p.heads + 2 * p.kv_heads;
-    using VI = Vec<TI, VEC>;
-    using VO = Vec<TO, VEC>;
-    for (int h0 = blockIdx.y * p.slots * kRopeHeads + slot; h0 < all; h0 += gridDim.y * p.slots * kRopeHeads) {
-        VI a[kRopeHeads], b[kRopeHeads];
 #pragma unroll
-        for (int j = 0; j < kRopeHeads; ++j) {
-            const int h = h0 + j * p.slots;
-            if (h < all) {
-                const TI *src = x + static_cast<int64_t>(h) * p.head_dim;
-                a[j] = *reinterpret_cast<const VI *>(src + off_a);
-                if (has_b) b[j] = *reinterpret_cast<const VI *>(src + off_b);
-            }
+    for (int j = 0; j < HEADS; ++j) {
+        const int h = h0 + j * p.slots;
+        if (h >= all) continue;
+        TO *dst = y + static_cast<int64_t>(h) * p.head_dim;
+        if (APPEND && h >= p.heads) {
+            const int kh = h - p.heads;
+            dst = kh < p.kv_heads ? static_cast<TO *>(p.k) + cache_row + kh * p.head_stride
+                                  : static_cast<TO *>(p.v) + cache_row + (kh - p.kv_heads) * p.head_stride;
         }
+        VO u[NV];
+        if (turns && !(APPEND && h >= p.heads + p.kv_heads)) {
 #pragma unroll
-        for (int j = 0; j < kRopeHeads; ++j) {
-            const int h = h0 + j * p.slots;
-            if (h >= all) continue;
-            TO *dst = y + static_cast<int64_t>(h) * p.head_dim;
-            if (APPEND && h >= p.heads) {
-                const int kh = h - p.heads;
-                dst = kh < p.kv_heads ? static_cast<TO *>(p.k) + cache_row + kh * p.head_stride
-                                      : static_cast<TO *>(p.v) + cache_row + (kh - p.kv_heads) * p.head_stride;
+            for (int i = 0; i < PAIRS; ++i) {
+                // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved)
+                const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
+                const float fa = widen(v[j][ea / VEC].v[ea % VEC]), fb = widen(v[j][eb / VEC].v[eb % VEC]);
+                u[ea / VEC].v[ea % VEC] = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
+                u[eb / VEC].v[eb % VEC] = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
             }
-            VO u, w;
-            if (turns && !(APPEND && h >= p.heads + p.kv_heads)) {
+        } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved)
-                    float fa, fb;
-                    if (INTERLEAVED) {
-                        fa = widen(2 * i < VEC ? a[j].v[(2 * i) % VEC] : b[j].v[(2 * i) % VEC]);
-                        fb = widen(2 * i + 1 < VEC ? a[j].v[(2 * i + 1) % VEC] : b[j].v[(2 * i + 1) % VEC]);
-                    } else {
-                        fa = widen(a[j].v[i]);
-                        fb = widen(b[j].v[i]);
-                    }
-                    const TO ra = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
-                    const TO rb = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
-                    if (INTERLEAVED) {
-                        if (2 * i < VEC) u.v[(2 * i) % VEC] = ra; else w.v[(2 * i) % VEC] = ra;
-                        if (2 * i + 1 < VEC) u.v[(2 * i + 1) % VEC] = rb; else w.v[(2 * i + 1) % VEC] = rb;
-                    } else {
-                        u.v[i] = ra;
-                        w.v[i] = rb;
-                    }
-                }
-            } else {
+            for (int n = 0; n < NV; ++n)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    u.v[i] = narrow<TO>(widen(a[j].v[i]));
-                    w.v[i] = has_b ? narrow<TO>(widen(b[j].v[i])) : u.v[i];
-                }
-            }
-            *reinterpret_cast<VO *>(dst + off_a) = u;
-            if (has_b) *reinterpret_cast<VO *>(dst + off_b) = w;
+                for (int i = 0; i < VEC; ++i) u[n].v[i] = narrow<TO>(widen(v[j][n].v[i]));
         }
+        *reinterpret_cast<VO *>(dst + off[0]) = u[0];
+        if (has1) *reinterpret_cast<VO *>(dst + off[1]) = u[NV - 1];
     }
 }
 
@@ -177,7 +189,7 @@ bool fits(const RopeParams &p, int vec, int in_size, int out_size, bool interlea
         return (reinterpret_cast<uintptr_t>(q) & static_cast<uintptr_t>(n - 1)) == 0;
     };
     if (p.head_dim % vec || p.rot % vec || p.ldx % vec || p.ldy % vec) return false;
-    if (interleaved ? p.rot % (2 * vec) : (p.rot / 2) % vec) return false;
+    if (!interleaved && (p.rot / 2) % vec) return false;
     if (!on(p.x, in_size) || !on(p.y, out_size)) return false;
     if (append && (p.page_stride % vec || p.head_stride % vec || p.row_stride % vec || !on(p.k, out_size) || !on(p.v, out_size)))
         return false;
@@ -186,15 +198,15 @@ bool fits(const RopeParams &p, int vec, int in_size, int out_size, bool interlea
 
 template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
 cudaError_t go(RopeParams p, cudaStream_t s) {
-    const int half = p.rot / 2;
+    constexpr int NV = kVectors<VEC, INTERLEAVED>, HEADS = kHeads<TI, VEC, INTERLEAVED>;
     const int all = p.heads + 2 * p.kv_heads;
-    p.places = half / VEC + (p.head_dim - p.rot + 2 * VEC - 1) / (2 * VEC);
-    int slots = 256 / p.places;
-    if (slots < 1) slots = 1;
-    if (slots > all) slots = all;
+    p.places = p.rot / (NV * VEC) + (p.head_dim - p.rot + NV * VEC - 1) / (NV * VEC);
+    p.table_vec = p.rot % 4 == 0 && (reinterpret_cast<uintptr_t>(p.table) & 15) == 0;
+    // many rows: each thread takes as many heads as it can hold; few rows: one head per thread where that fits a CTA
+    int slots = p.T >= 2 * num_sms() ? (all + HEADS - 1) / HEADS : all;
+    if (slots > 256 / p.places) slots = 256 / p.places;
     p.slots = slots;
-    // one round of heads per CTA: rows with few tokens still spread over the SMs
-    const int rounds = (all + slots * kRopeHeads - 1) / (slots * kRopeHeads);
+    const int rounds = (all + slots * HEADS - 1) / (slots * HEADS);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -210,7 +222,9 @@ cudaError_t go(RopeParams p, cudaStream_t s) {
 template <typename TI, typename TO, bool INTERLEAVED, bool APPEND>
 cudaError_t by_vec(const RopeParams &p, cudaStream_t s) {
     const int in = sizeof(TI), out = sizeof(TO);
-    if (fits(p, 8, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 8, INTERLEAVED, APPEND>(p, s);
+    if constexpr (sizeof(TI) == 2) {   // 16 bytes of a row at most
+        if (fits(p, 8, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 8, INTERLEAVED, APPEND>(p, s);
+    }
     if (fits(p, 4, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 4, INTERLEAVED, APPEND>(p, s);
     if (fits(p, 2, in, out, INTERLEAVED, APPEND)) return go<TI, TO, 2, INTERLEAVED, APPEND>(p, s);
     return go<TI, TO, 1, INTERLEAVED, APPEND>(p, s);
