@@ -60,13 +60,13 @@ struct RopeParams {
 // vectors of a head that one thread holds: both halves of its pairs, or (interleaved) one vector of whole pairs
 template <int VEC, bool INTERLEAVED>
 constexpr int kVectors = INTERLEAVED && VEC > 1 ? 1 : 2;
-// heads per thread: 128 bytes of a row in flight, at most 8
+// heads per thread: 64 bytes of a row, at most 4 heads (32 to 128 bytes with 3 to 8 CTAs per SM measured)
 template <typename TI, int VEC, bool INTERLEAVED>
-constexpr int kHeads = 128 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) < 8
-                           ? 128 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) : 8;
+constexpr int kHeads = 64 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) < 4
+                           ? 64 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) : 4;
 
 template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
+__global__ void __launch_bounds__(256, 4) k_rope(const RopeParams p) {
     constexpr int NV = kVectors<VEC, INTERLEAVED>, HEADS = kHeads<TI, VEC, INTERLEAVED>;
     constexpr int PAIRS = NV * VEC / 2;
     using VI = Vec<TI, VEC>;
@@ -165,7 +165,9 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
         if (turns && !(APPEND && h >= p.heads + p.kv_heads)) {
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
-                // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved)
+                // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved).  Scalar
+                // operations: the paired ones (f32x2) are joined into a fused multiply-add by the compiler, in PTX
+                // with .rn too, which rounds once less.
                 const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
                 const float fa = widen(v[j][ea / VEC].v[ea % VEC]), fb = widen(v[j][eb / VEC].v[eb % VEC]);
                 u[ea / VEC].v[ea % VEC] = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
