@@ -32,6 +32,13 @@ __device__ __forceinline__ float narrow<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// a feature that is not turned: as it is, or rounded to the narrower type
+template <typename TO, typename TI>
+__device__ __forceinline__ TO copied(TI x) {
+    if constexpr (sizeof(TI) == sizeof(TO)) return x;
+    else return narrow<TO>(widen(x));
+}
+
 struct RopeParams {
     const void *x;            // input rows
     int64_t ldx;
@@ -47,6 +54,7 @@ struct RopeParams {
     int table_vec;            // table rows lie on 16 bytes
     int places;               // threads per head
     int slots;                // heads a CTA holds at once
+    uint32_t row_bytes, slot_bytes;   // of the ring: a row's features, a slot
     // append
     void *k, *v;
     int64_t page_stride, head_stride, row_stride;
@@ -177,10 +185,202 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeParams p) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) u[n].v[i] = narrow<TO>(widen(v[j][n].v[i]));
+                for (int i = 0; i < VEC; ++i) u[n].v[i] = copied<TO>(v[j][n].v[i]);
         }
         *reinterpret_cast<VO *>(dst + off[0]) = u[0];
         if (has1) *reinterpret_cast<VO *>(dst + off[1]) = u[NV - 1];
+    }
+}
+
+// ---------------------------------------------------------------- many rows
+//
+// A persistent CTA takes rows blockIdx.x, + gridDim.x, ...: one producer warp brings whole rows and their rows of the
+// table into a ring in shared memory (bulk copies counted on an mbarrier) and looks up their places in the cache,
+// eight warps turn them and write them out.  What a CTA per row waits for one after the other (its start, the
+// position, the page, the features) then lies behind the rows before it: with 4084 rows of 96 heads of 128 the direct
+// form above takes 48 us, whatever its share of registers and loads in flight.
+constexpr int kRowWarps = 8;
+constexpr int kRowSlots = 3;
+
+struct RowInfo {
+    int64_t at;   // place in the cache
+    int pos;      // or -1: nothing is written for this row
+};
+struct RowShared {
+    uint64_t full[kRowSlots], empty[kRowSlots];
+    RowInfo info[kRowSlots];
+    int abort;
+};
+
+template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
+__global__ void __launch_bounds__((kRowWarps + 1) * 32) k_rope_rows(const RopeParams p) {
+    constexpr int NV = kVectors<VEC, INTERLEAVED>;
+    constexpr int PAIRS = NV * VEC / 2;
+    using VI = Vec<TI, VEC>;
+    using VO = Vec<TO, VEC>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    RowShared &sh = *reinterpret_cast<RowShared *>(smem + kRowSlots * static_cast<size_t>(p.slot_bytes));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRowSlots; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kRowWarps);
+        }
+        fence_mbar_init();
+        sh.abort = 0;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = p.rot >> 1, table_bytes = half * 8;
+
+    if (warp == kRowWarps) {   // producer: its lanes look up 32 rows at a time, lane 0 copies them in turn
+        int slot = 0, round = 0;
+        // no copy may outlive the CTA, after a wait that ran out least of all: wait for the last one into each slot
+        auto drain = [&]() {
+            if (lane == 0) {
+                for (int i = 0; i < kRowSlots; ++i) {
+                    const int last = i < slot ? round : round - 1;
+                    int own = 0;
+                    if (last >= 0) mbar_wait_bounded(&sh.full[i], last & 1, &own, p.status);
+                }
+            }
+            __syncwarp();
+        };
+        for (int64_t t0 = blockIdx.x; t0 < p.T; t0 += 32ll * gridDim.x) {
+            const int64_t mine = t0 + static_cast<int64_t>(lane) * gridDim.x;
+            int pos = -1;
+            int64_t at = 0;
+            if (mine < p.T) {
+                pos = __ldg(p.pos + mine);
+                int64_t seq = mine;
+                if (APPEND && p.seq) seq = __ldg(p.seq + mine);
+                if (APPEND && seq < 0) pos = -1;   // a padding row, like one of a negative position
+                if (pos >= 0) {
+                    bool bad = p.rot > 0 && pos >= p.n_pos;
+                    if (APPEND) {
+                        const int64_t in_table = pos >> p.page_shift;
+                        bad = bad || seq >= p.n_seqs || in_table >= p.max_pages;
+                        if (!bad) {
+                            const int64_t page = __ldg(p.pages + seq * p.max_pages + in_table);
+                            bad = page < 0 || page >= p.n_pages;
+                            at = page * p.page_stride + static_cast<int64_t>(pos & ((1 << p.page_shift) - 1)) * p.row_stride;
+                        }
+                    }
+                    if (bad) {
+                        atomicOr(p.status, kStatusBadIndex);
+                        pos = -1;
+                    }
+                }
+            }
+            for (int k = 0; k < 32; ++k) {
+                const int64_t t = t0 + static_cast<int64_t>(k) * gridDim.x;
+                if (t >= p.T) break;
+                const int row_pos = __shfl_sync(0xffffffffu, pos, k);
+                const int64_t row_at = __shfl_sync(0xffffffffu, at, k);
+                bool ok = true;
+                if (lane == 0) {
+                    if (round > 0) ok = mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1, &sh.abort, p.status);
+                    if (ok) {
+                        uint8_t *to = smem + slot * static_cast<size_t>(p.slot_bytes);
+                        sh.info[slot].at = row_at;
+                        sh.info[slot].pos = row_pos;
+                        const uint32_t bytes = row_pos >= 0 ? p.row_bytes + table_bytes : 0;
+                        mbar_arrive_expect_tx(&sh.full[slot], bytes);   // also releases the row's info
+                        if (row_pos >= 0) {
+                            bulk_load(to, static_cast<const uint8_t *>(p.x) + t * p.ldx * static_cast<int64_t>(sizeof(TI)), p.row_bytes, &sh.full[slot]);
+                            if (table_bytes) bulk_load(to + p.row_bytes, p.table + static_cast<int64_t>(row_pos) * half, table_bytes, &sh.full[slot]);
+                        }
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+                    drain();
+                    return;
+                }
+                if (++slot == kRowSlots) {
+                    slot = 0;
+                    ++round;
+                }
+            }
+        }
+        drain();
+        return;
+    }
+
+    const int place = threadIdx.x % p.places, first = threadIdx.x / p.places;
+    const bool works = first < p.slots;
+    const int turned = half / PAIRS;   // places that rotate
+    const bool turns = place < turned;
+    int off[2];
+    if (turns) {
+        off[0] = INTERLEAVED ? NV * VEC * place : VEC * place;
+        off[1] = INTERLEAVED ? off[0] + VEC : half + off[0];
+    } else {
+        off[0] = p.rot + NV * VEC * (place - turned);
+        off[1] = off[0] + VEC;
+    }
+    const bool has1 = NV == 2 && off[1] < p.head_dim;   // an odd count of copied vectors leaves the last one alone
+    int slot = 0, round = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (!mbar_wait_bounded(&sh.full[slot], round & 1, &sh.abort, p.status)) return;
+        const uint8_t *from = smem + slot * static_cast<size_t>(p.slot_bytes);
+        const RowInfo info = sh.info[slot];
+        if (info.pos >= 0 && works) {
+            float c[PAIRS], s[PAIRS];
+            if (turns) {
+                const float2 *cs = reinterpret_cast<const float2 *>(from + p.row_bytes) + PAIRS * place;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    c[i] = cs[i].x;
+                    s[i] = p.inverse ? -cs[i].y : cs[i].y;
+                }
+            }
+            const TI *row = reinterpret_cast<const TI *>(from);
+            // heads first, + slots, ... of n heads from `src` on, to dst + head * stride
+            auto heads = [&](const TI *src, int n, TO *dst, int64_t stride, bool turn) {
+                src += first * p.head_dim;
+                dst += first * stride;
+                const int src_step = p.slots * p.head_dim;
+                const int64_t dst_step = p.slots * stride;
+#pragma unroll 4
+                for (int h = first; h < n; h += p.slots) {
+                    VI v[NV];
+                    VO w[NV];
+                    v[0] = *reinterpret_cast<const VI *>(src + off[0]);
+                    if (has1) v[NV - 1] = *reinterpret_cast<const VI *>(src + off[1]);
+                    if (turn) {
+#pragma unroll
+                        for (int i = 0; i < PAIRS; ++i) {
+                            const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
+                            const float fa = widen(v[ea / VEC].v[ea % VEC]), fb = widen(v[eb / VEC].v[eb % VEC]);
+                            w[ea / VEC].v[ea % VEC] = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
+                            w[eb / VEC].v[eb % VEC] = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) w[i].v[e] = copied<TO>(v[i].v[e]);
+                    }
+                    *reinterpret_cast<VO *>(dst + off[0]) = w[0];
+                    if (has1) *reinterpret_cast<VO *>(dst + off[1]) = w[NV - 1];
+                    src += src_step;
+                    dst += dst_step;
+                }
+            };
+            heads(row, p.heads, static_cast<TO *>(p.y) + t * p.ldy, p.head_dim, turns);
+            if (APPEND) {
+                const TI *k = row + static_cast<int64_t>(p.heads) * p.head_dim;
+                heads(k, p.kv_heads, static_cast<TO *>(p.k) + info.at, p.head_stride, turns);
+                heads(k + static_cast<int64_t>(p.kv_heads) * p.head_dim, p.kv_heads, static_cast<TO *>(p.v) + info.at, p.head_stride, false);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        if (++slot == kRowSlots) {
+            slot = 0;
+            ++round;
+        }
     }
 }
 
@@ -208,6 +408,36 @@ cudaError_t go(RopeParams p, cudaStream_t s) {
     int slots = p.T >= 2 * num_sms() ? (all + HEADS - 1) / HEADS : all;
     if (slots > 256 / p.places) slots = 256 / p.places;
     p.slots = slots;
+    // Rows by the ring: enough of them for every CTA to have several, and whole 16-byte pieces in a row and in the
+    // table's; three rows have to leave room for two CTAs.
+    const int64_t row_bytes = static_cast<int64_t>(all) * p.head_dim * static_cast<int64_t>(sizeof(TI));
+    const int64_t slot_bytes = (row_bytes + p.rot * 4 + 127) / 128 * 128;
+    const int64_t smem = kRowSlots * slot_bytes + static_cast<int64_t>(sizeof(RowShared));
+    // Measured (direct / ring, us): 4084 cache rows of 96 heads of 128 48.4 / 42.5, of 100 63.8 / 41.5; 2048 rows of 64
+    // heads of 100 12.4 / 10.1; but 4095 fp32 rows of 64 x 128 41.3 / 46.6: rotation alone in 16-byte vectors stays direct.
+    if ((APPEND || VEC * sizeof(TI) < 16) && p.T >= 8 * num_sms() && smem <= 113 * 1024 && row_bytes % 16 == 0 && p.ldx * sizeof(TI) % 16 == 0 &&
+        (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.rot % 4 == 0 && (reinterpret_cast<uintptr_t>(p.table) & 15) == 0) {
+        p.row_bytes = static_cast<uint32_t>(row_bytes);
+        p.slot_bytes = static_cast<uint32_t>(slot_bytes);
+        p.slots = 32 * kRowWarps / p.places;
+        const void *f = reinterpret_cast<const void *>(k_rope_rows<TI, TO, VEC, INTERLEAVED, APPEND>);
+        cudaError_t e = smem_attr(f, 113 * 1024);
+        if (e != cudaSuccess) return e;
+        int64_t per_sm = 226 * 1024 / (smem + 1024);
+        if (per_sm > 6) per_sm = 6;   // 288 threads each
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        const int64_t grid = per_sm * num_sms();
+        cfg.gridDim = dim3(static_cast<unsigned>(grid < p.T ? grid : p.T));
+        cfg.blockDim = dim3((kRowWarps + 1) * 32);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, k_rope_rows<TI, TO, VEC, INTERLEAVED, APPEND>, p);
+    }
     const int rounds = (all + slots * HEADS - 1) / (slots * HEADS);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

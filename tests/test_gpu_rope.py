@@ -266,3 +266,43 @@ def test_refusals(bn):
     with pytest.raises(bn.BitnetError):                    # rows that do not lie on 16 bytes
         W = torch.zeros((2, 4, 1, 16, 68), dtype=BF16, device="cuda")[..., :64]
         bn.bitnet_rope_append(x[:2], pos[:2], tab, W[0], W[1], pages)
+
+
+@pytest.mark.parametrize("heads,kv,d,rot", [(32, 32, 100, 100), (20, 5, 128, 128), (6, 2, 40, 24), (2, 1, 72, 0), (4, 4, 36, 20)])
+@pytest.mark.parametrize("dtype,interleaved,layout", [(BF16, False, "heads first"), (F32, True, "rows first"), (BF16, True, "rows first")])
+def test_append_of_many_rows(bn, heads, kv, d, rot, dtype, interleaved, layout):
+    """Enough rows for several per persistent CTA, with padding rows and rows of bad indexes among them."""
+    new = 701
+    x, pos, seq, pages, tab, K, V = _append_case(bn, heads, kv, d, rot, dtype, interleaved, 32, [3, 500], new, layout, d)
+    r = np.random.default_rng(d)
+    odd = r.choice(len(pos), 40, replace=False)
+    pos[odd[:10]] = -1
+    seq[odd[10:20]] = -2
+    seq[odd[20:30]] = 2 + r.integers(0, 1000, 10)
+    pos[odd[30:]] = 10 ** 6 + r.integers(0, 1000, 10)
+    good = np.ones(len(pos), bool)
+    good[odd] = False
+    Qr, Kr, Vr = _append_ref(x, np.where(good, pos, -1), np.where(good, seq, 0), pages, tab, K, V, heads, kv, d, interleaved)
+    Q = torch.full((len(pos), heads * d), 7.0, dtype=BF16, device="cuda")
+    ws = bn.Workspace(256)
+    bn.bitnet_rope_append(up(x, dtype), up(pos, torch.int32), None if tab is None else up(tab), K, V, up(pages, torch.int32),
+                          seq=up(seq, torch.int32), interleaved=interleaved, Q=Q, ws=ws)
+    assert bn.bitnet_read_device_status(ws) == bn._abi.BITNET_ERR_INVALID_ARG
+    assert np.array_equal(host(Q)[good], Qr[good]) and bool((Q[torch.from_numpy(~good).cuda()] == 7.0).all())
+    assert np.array_equal(host(K), Kr) and np.array_equal(host(V), Vr)
+
+
+@pytest.mark.parametrize("d,rot", [(100, 100), (100, 36), (128, 128), (50, 20)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rope_of_many_rows_in_place(bn, d, rot, dtype):
+    T, heads = 1500, 8
+    r = np.random.default_rng(d + rot)
+    x = r.normal(size=(T, heads * d)).astype(np.float32)
+    x = bf16(x) if dtype == BF16 else x
+    pos = r.integers(-3, 2000, T).astype(np.int32)
+    tab = table_ref(2000, rot)
+    ref = turn(x.reshape(T, heads, d), tab[np.maximum(pos, 0)], False).reshape(T, -1)
+    ref = np.where(pos[:, None] >= 0, bf16(ref) if dtype == BF16 else ref, x)
+    xd = up(x, dtype)
+    bn.bitnet_rope(xd, up(pos, torch.int32), up(tab), heads, Y=xd)
+    assert np.array_equal(host(xd).view(np.uint32), ref.view(np.uint32))
