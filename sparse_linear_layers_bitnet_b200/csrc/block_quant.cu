@@ -417,13 +417,14 @@ __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
 template <int CPT, bool ADD>
 __global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *X, const uint4 *R, uint4 *H,
                                                          const float4 *__restrict__ w,
-                                                         int K, float eps_n, float eps_a,
+                                                         int K, double inv_k, float eps_n, float eps_a,
                                                          int8_t *__restrict__ Xq, float *__restrict__ amax,
                                                          float *__restrict__ rinv) {
     __shared__ unsigned long long s_bins[kSqBins];
     __shared__ unsigned long long s_lo[8], s_hi[8];
     __shared__ uint32_t s_limb[kSqLimbs];
     __shared__ float s_red[8];
+    __shared__ double s_sq[8];
     __shared__ float s_r;
     const int64_t t = blockIdx.x;
     const int nchunk = K >> 3;
@@ -452,60 +453,92 @@ __global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *X, const 
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    uint64_t lo = 0, hi = 0;
-    bool rare = false;
+    // S by fp64 fused multiply-adds.  At most 64 of them per thread, 5 steps in a warp and 8 over the warps: the sum is
+    // within 2^-46 of the exact one, and so are 1/K and the product.  Where everything within 2^-44 of the quotient
+    // rounds to the same fp32 (all but one row in 2^19), that is ms; else, and for tiny rows (zeros and subnormals are
+    // taken as about 2^-127 here), the exact sum below decides.
+    double sq = 0.0;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
-        if (!sq_chunk_f64(v[j], lo, hi)) {   // a wide or out-of-window chunk: value by value
-            const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        double s0 = 0.0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                rare |= sq_window(wv[e] & 0xffffu, lo, hi);
-                rare |= sq_window(wv[e] >> 16, lo, hi);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const double x0 = bf16abs_f64((wv[e] & 0x7fffu) << 13), x1 = bf16abs_f64((wv[e] >> 3) & 0x0fffe000u);
+            s0 = __fma_rn(x0, x0, s0);
+            sq = __fma_rn(x1, x1, sq);
         }
+        sq += s0;
     }
-    const bool any_rare = __syncthreads_or(rare) != 0;
-    if (any_rare) {   // squares outside the window go to per-exponent bins (a second scan of the registers)
-        for (int i = threadIdx.x; i < kSqBins; i += blockDim.x) s_bins[i] = 0ull;
-        __syncthreads();
-        if (rare) {
 #pragma unroll
-            for (int j = 0; j < CPT; ++j) {
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) s_sq[warp] = sq;
+    __syncthreads();
+    sq = s_sq[0];
+    for (int i = 1; i < nw; ++i) sq += s_sq[i];
+    const double q = sq * inv_k;
+    float ms = __double2float_rn(q * (1.0 - 0x1p-44));
+    const bool sure = q > 0x1p-120 && ms == __double2float_rn(q * (1.0 + 0x1p-44));
+    float r;
+    if (sure) {   // the same for every thread
+        r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
+        if (rinv && threadIdx.x == 0) rinv[t] = r;
+    } else {
+        uint64_t lo = 0, hi = 0;
+        bool rare = false;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            if (!sq_chunk_f64(v[j], lo, hi)) {   // a wide or out-of-window chunk: value by value
                 const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sq_rare_add(wv[e] & 0xffffu, s_bins);
-                    sq_rare_add(wv[e] >> 16, s_bins);
+                    rare |= sq_window(wv[e] & 0xffffu, lo, hi);
+                    rare |= sq_window(wv[e] >> 16, lo, hi);
                 }
             }
         }
-    }
+        const bool any_rare = __syncthreads_or(rare) != 0;
+        if (any_rare) {   // squares outside the window go to per-exponent bins (a second scan of the registers)
+            for (int i = threadIdx.x; i < kSqBins; i += blockDim.x) s_bins[i] = 0ull;
+            __syncthreads();
+            if (rare) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
-        add128_sq(lo, hi, l2, h2);
-    }
-    if (lane == 0) {
-        s_lo[warp] = lo;
-        s_hi[warp] = hi;
-    }
-    __syncthreads();
-    if (warp == 0) {   // one warp forms the total and r (its lanes in step), the others wait at the barrier
-        uint64_t L = 0, H = 0;
-        for (int i = 0; i < nw; ++i) add128_sq(L, H, s_lo[i], s_hi[i]);
-        double S;
-        if (!any_rare) S = window_to_f64(L, H);
-        else S = lane == 0 ? sq_finalize(L, H, s_bins, true, s_limb) : 0.0;
-        if (lane == 0) {
-            const float ms = __double2float_rn(__ddiv_rn(S, static_cast<double>(K)));
-            const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
-            s_r = r;
-            if (rinv) rinv[t] = r;
+                for (int j = 0; j < CPT; ++j) {
+                    const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sq_rare_add(wv[e] & 0xffffu, s_bins);
+                        sq_rare_add(wv[e] >> 16, s_bins);
+                    }
+                }
+            }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+            add128_sq(lo, hi, l2, h2);
+        }
+        if (lane == 0) {
+            s_lo[warp] = lo;
+            s_hi[warp] = hi;
+        }
+        __syncthreads();
+        if (warp == 0) {   // one warp forms the total and r (its lanes in step), the others wait at the barrier
+            uint64_t L = 0, H = 0;
+            for (int i = 0; i < nw; ++i) add128_sq(L, H, s_lo[i], s_hi[i]);
+            double S;
+            if (!any_rare) S = window_to_f64(L, H);
+            else S = lane == 0 ? sq_finalize(L, H, s_bins, true, s_limb) : 0.0;
+            if (lane == 0) {
+                const float ms = __double2float_rn(__ddiv_rn(S, static_cast<double>(K)));
+                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
+                s_r = r;
+                if (rinv) rinv[t] = r;
+            }
+        }
+        __syncthreads();
+        r = s_r;
     }
-    __syncthreads();
-    const float r = s_r;
     float xn[CPT][8];
     float m = 0.0f;
 #pragma unroll
@@ -668,7 +701,8 @@ static cudaError_t rms_rc(cudaLaunchConfig_t &cfg, const void *X, const void *R,
                           float eps_n, float eps_a, int8_t *Xq, float *amax, float *rinv) {
     return cudaLaunchKernelEx(&cfg, k_rmsnorm_quant_rc<CPT, ADD>, static_cast<const uint4 *>(X),
                               static_cast<const uint4 *>(R), static_cast<uint4 *>(H),
-                              reinterpret_cast<const float4 *>(w), static_cast<int>(K), eps_n, eps_a, Xq, amax, rinv);
+                              reinterpret_cast<const float4 *>(w), static_cast<int>(K),
+                              1.0 / static_cast<double>(K), eps_n, eps_a, Xq, amax, rinv);
 }
 
 template <bool ADD>
