@@ -34,21 +34,34 @@ __device__ __forceinline__ void load8(const float *row, int c, float *f) {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
-// the same through the coherent path, for a row that the kernel writes (dH may be dR)
-__device__ __forceinline__ void load8_rw(const __nv_bfloat16 *row, int c, float *f) {
-    const uint4 u = reinterpret_cast<const uint4 *>(row)[c];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// the same in two steps: eight values as they lie in memory (plain loads: dH may be dR), and their fp32 values
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int c) { u = reinterpret_cast<const uint4 *>(row)[c]; }
+    __device__ __forceinline__ void widen(float *f) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8_rw(const float *row, int c, float *f) {
-    const float4 a = reinterpret_cast<const float4 *>(row)[2 * c], b = reinterpret_cast<const float4 *>(row)[2 * c + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *row, int c) {
+        a = reinterpret_cast<const float4 *>(row)[2 * c];
+        b = reinterpret_cast<const float4 *>(row)[2 * c + 1];
+    }
+    __device__ __forceinline__ void widen(float *f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -79,23 +92,46 @@ __global__ void __launch_bounds__(512) k_rmsnorm_grad(const TY *__restrict__ dY,
     for (int j = 0; j < CPT; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-    int flip = 0;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    // the next row is on its way while this one is worked on (with up to two chunks a thread: more do not fit the registers)
+    constexpr bool kAhead = CPT <= 2;
+    Raw8<TY> ny[CPT];
+    Raw8<__nv_bfloat16> nh[CPT];
+    Raw8<TG> nr[CPT];
+    float next_r = 0.0f;
+    auto fetch = [&](int t) {
         const int64_t base = static_cast<int64_t>(t) * K;
-        const float r = __ldg(rinv + t);
-        float e[CPT][8], u[CPT][8];
-        float dot = 0.0f;
+        next_r = __ldg(rinv + t);
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             if (c < nchunk) {
-                load8(dY + base, c, e[j]);
-                load8(H + base, c, u[j]);
+                ny[j].load(dY + base, c);
+                nh[j].load(H + base, c);
+                if (dR) nr[j].load(dR + base, c);
+            }
+        }
+    };
+    if (kAhead && static_cast<int>(blockIdx.x) < T) fetch(blockIdx.x);
+    int flip = 0;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        const int64_t base = static_cast<int64_t>(t) * K;
+        if (!kAhead) fetch(t);
+        const float r = next_r;
+        float e[CPT][8], u[CPT][8];
+        Raw8<TG> res[CPT];
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            if (static_cast<int>(threadIdx.x + j * blockDim.x) < nchunk) {
+                ny[j].widen(e[j]);
+                nh[j].widen(u[j]);
+                res[j] = nr[j];
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e[j][i] = u[j][i] = 0.0f;
             }
         }
+        if (kAhead && t + static_cast<int>(gridDim.x) < T) fetch(t + gridDim.x);
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
@@ -132,7 +168,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_grad(const TY *__restrict__ dY,
                 for (int i = 0; i < 8; ++i) d[i] = r * fmaf(-u[j][i], sum, e[j][i]);
                 if (dR) {
                     float q[8];
-                    load8_rw(dR + base, c, q);
+                    res[j].widen(q);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) d[i] += q[i];
                 }
@@ -188,7 +224,9 @@ __global__ void __launch_bounds__(512) k_rmsnorm_grad_long(const TY *__restrict_
         for (int i = 0; i < 8; ++i) d[i] = r * fmaf(-(u[i] * r), sum, w ? e[i] * wv[i] : e[i]);
         if (dR) {
             float q[8];
-            load8_rw(dR + base, c, q);
+            Raw8<TG> raw;
+            raw.load(dR + base, c);
+            raw.widen(q);
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] += q[i];
         }
@@ -238,8 +276,6 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_dw_sum(const float *__restrict
     }
 }
 
-constexpr int kGradMaxChunks = 512 * 4;   // chunks of a row the register form holds
-
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
     cudaLaunchAttribute attr[1];
@@ -254,28 +290,37 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-int partial_rows(int64_t T) {
-    const int64_t most = 2 * static_cast<int64_t>(num_sms());
+// Chunks per thread and threads of the row kernel (0 chunks: rows too long for it).
+int chunks_per_thread(int64_t nchunk, int *threads) {
+    const int cpt = nchunk <= 512 ? 1 : nchunk <= 1024 ? 2 : nchunk <= 1536 ? 3 : 0;
+    *threads = cpt ? static_cast<int>((nchunk + cpt - 1) / cpt + 31) / 32 * 32 : 512;
+    return cpt;
+}
+
+// CTAs of the row kernel, each with a partial dw row: about 1024 threads per SM, two CTAs at least and eight at most
+// (more of them cost more in partial rows than they hide: 4 instead of 2 per SM at K = 4096 53.1 against 48.8 us).
+int partial_rows(int64_t T, int64_t K) {
+    int threads;
+    chunks_per_thread(K / 8, &threads);
+    int per_sm = 1024 / threads;
+    per_sm = per_sm < 2 ? 2 : per_sm > 8 ? 8 : per_sm;
+    const int64_t most = static_cast<int64_t>(per_sm) * num_sms();
     return static_cast<int>(T < most ? T : most);
 }
 
 template <typename TY, typename TG>
 cudaError_t grad_launch(const TY *dY, const __nv_bfloat16 *H, const float *w, const float *rinv, const TG *dR, int T, int K,
                         TG *dH, float *dwp, cudaStream_t s) {
-    const int nchunk = K / 8;
-    const int rows = partial_rows(T);
-    if (nchunk > kGradMaxChunks) {
-        cudaError_t e = launch_pdl(k_rmsnorm_grad_long<TY, TG>, dim3(T), dim3(512), s, dY, H, w, rinv, dR, dH, K);
-        if (e != cudaSuccess || !dwp) return e;
-        return launch_pdl(k_rmsnorm_dw<TY>, dim3((nchunk + 255) / 256, rows), dim3(256), s, dY, H, rinv, dwp, T, K);
-    }
-    const int cpt = nchunk <= 512 ? 1 : nchunk <= 1024 ? 2 : 4;
-    const int threads = ((nchunk + cpt - 1) / cpt + 31) / 32 * 32;
-    switch (cpt) {
+    const int nchunk = K / 8, rows = partial_rows(T, K);
+    int threads;
+    switch (chunks_per_thread(nchunk, &threads)) {
         case 1: return launch_pdl(k_rmsnorm_grad<TY, TG, 1>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
         case 2: return launch_pdl(k_rmsnorm_grad<TY, TG, 2>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
-        default: return launch_pdl(k_rmsnorm_grad<TY, TG, 4>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
+        case 3: return launch_pdl(k_rmsnorm_grad<TY, TG, 3>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
     }
+    cudaError_t e = launch_pdl(k_rmsnorm_grad_long<TY, TG>, dim3(T), dim3(512), s, dY, H, w, rinv, dR, dH, K);
+    if (e != cudaSuccess || !dwp) return e;
+    return launch_pdl(k_rmsnorm_dw<TY>, dim3((nchunk + 255) / 256, rows), dim3(256), s, dY, H, rinv, dwp, T, K);
 }
 
 }  // namespace
@@ -283,7 +328,7 @@ cudaError_t grad_launch(const TY *dY, const __nv_bfloat16 *H, const float *w, co
 // status word, then one partial dw row per CTA of the row kernel
 size_t rmsnorm_grad_ws_bytes(int64_t T, int64_t K) {
     if (T <= 0 || K <= 0) return 256;
-    return static_cast<size_t>(partial_rows(T)) * static_cast<size_t>(K) * 4 + 256;
+    return static_cast<size_t>(partial_rows(T, K)) * static_cast<size_t>(K) * 4 + 256;
 }
 
 cudaError_t launch_rmsnorm_grad(const void *dY, bool dy_bf16, const void *H, const float *w, const float *rinv,
@@ -303,7 +348,7 @@ cudaError_t launch_rmsnorm_grad(const void *dY, bool dy_bf16, const void *H, con
                    : grad_launch(g, h, w, rinv, static_cast<const float *>(dR), t, k, static_cast<float *>(dH), dwp, s);
     }
     if (e != cudaSuccess || !dw) return e;
-    return launch_pdl(k_rmsnorm_dw_sum, dim3((k + 31) / 32), dim3(32, 32), s, dwp, partial_rows(T), k, dw, accumulate ? 1 : 0);
+    return launch_pdl(k_rmsnorm_dw_sum, dim3((k + 31) / 32), dim3(32, 32), s, dwp, partial_rows(T, K), k, dw, accumulate ? 1 : 0);
 }
 
 }  // namespace bitnet
