@@ -78,10 +78,10 @@ __device__ __forceinline__ void store8(float *row, int c, const float *f) {
 // CPT chunks of 8 columns per thread; the row's K / 8 chunks lie at threadIdx.x
 // + j blockDim.x.  dwp: [gridDim.x, K] partial dw rows, or NULL.
 template <typename TY, typename TG, int CPT>
-__global__ void __launch_bounds__(512) k_rmsnorm_grad(const TY *__restrict__ dY, const __nv_bfloat16 *__restrict__ H,
+__global__ void __launch_bounds__(CPT == 2 ? 576 : 512) k_rmsnorm_grad(const TY *__restrict__ dY, const __nv_bfloat16 *__restrict__ H,
                                                       const float *__restrict__ w, const float *__restrict__ rinv,
                                                       const TG *dR, TG *dH, float *__restrict__ dwp, int T, int K) {
-    __shared__ float s_red[2][16];
+    __shared__ float s_red[2][32];
     const int nchunk = K >> 3;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const float inv_k = 1.0f / static_cast<float>(K);
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(512) k_rmsnorm_grad(const TY *__restrict__ dY,
         __syncthreads();   // two buffers: a warp reaches the next row's write only after all have passed this row's barrier
         float sum = lane < nw ? s_red[flip][lane] : 0.0f;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sum = __shfl_sync(0xffffffffu, sum, 0) * inv_k;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum *= inv_k;
         flip ^= 1;
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
@@ -292,7 +292,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
 
 // Chunks per thread and threads of the row kernel (0 chunks: rows too long for it).
 int chunks_per_thread(int64_t nchunk, int *threads) {
-    const int cpt = nchunk <= 512 ? 1 : nchunk <= 1024 ? 2 : nchunk <= 1536 ? 3 : 0;
+    const int cpt = nchunk <= 512 ? 1 : nchunk <= 1152 ? 2 : nchunk <= 1536 ? 3 : 0;
     *threads = cpt ? static_cast<int>((nchunk + cpt - 1) / cpt + 31) / 32 * 32 : 512;
     return cpt;
 }
