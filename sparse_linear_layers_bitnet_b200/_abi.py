@@ -184,9 +184,15 @@ def check(status: int, where: str) -> None:
 
 # ------------------------------------------------------------------ torch helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -199,17 +205,16 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _launch(name: str, like, stream, *args) -> None:
-    """Calls the entry point `name` with args and the stream, on the device of the
-    tensor `like`: the current stream of that device unless one is given."""
+def _launch(name: str, index: int, stream, *args) -> None:
+    """Calls the entry point `name` with args and the stream, on the device `index`:
+    the current stream of that device unless one is given."""
     torch = _torch()
-    index = like.get_device()
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return _launch(name, like, stream, *args)
+            return _launch(name, index, stream, *args)
     # the current stream's handle, without the Stream object that torch.cuda.current_stream() makes (5 us a call)
     raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-    status = getattr(load(), name)(*args, raw)
+    status = getattr(_lib if _lib is not None else load(), name)(*args, raw)
     if status != BITNET_OK:
         check(status, name)
 
@@ -243,11 +248,9 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _is(t, dtype, shape, like, optional=False) -> bool:
-    """t is a contiguous tensor of that type and shape on like's device (or None, where optional)."""
-    if t is None:
-        return optional
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == like.get_device()
+def _is(t, dtype, shape, index: int) -> bool:
+    """t is a contiguous tensor of that type and shape on the device `index`."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
 
 
 def _dtype_code(dt) -> int:
@@ -510,15 +513,16 @@ def bitnet_add_rmsnorm_quant(X, R, w=None, eps_norm: float = 1e-6, eps_act: floa
     Returns (H, Xq, absmax, rinv)."""
     torch = _torch()
     T, K = X.shape
-    assert _is(X, torch.bfloat16, (T, K), X) and X.is_cuda and _is(R, torch.bfloat16, (T, K), X)
-    assert _is(w, torch.float32, (K,), X, optional=True)
+    bf16, f32, rows, index = torch.bfloat16, torch.float32, (T, K), X.get_device()
+    assert X.is_cuda and _is(X, bf16, rows, index) and _is(R, bf16, rows, index)
+    assert w is None or _is(w, f32, (K,), index)
     H = _new((T, K), torch.bfloat16, X, stream) if H is None else H
     Xq = _new((T, K), torch.int8, X, stream) if Xq is None else Xq
     absmax = _new((T,), torch.float32, X, stream) if absmax is None else absmax
     rinv = _new((T,), torch.float32, X, stream) if rinv is None else rinv
-    assert _is(H, torch.bfloat16, (T, K), X) and _is(Xq, torch.int8, (T, K), X)
-    assert _is(absmax, torch.float32, (T,), X) and _is(rinv, torch.float32, (T,), X)
-    _launch("bitnet_add_rmsnorm_quant", X, stream, X.data_ptr(), R.data_ptr(), _addr(w), T, K, eps_norm, eps_act,
+    assert _is(H, bf16, rows, index) and _is(Xq, torch.int8, rows, index)
+    assert _is(absmax, f32, (T,), index) and _is(rinv, f32, (T,), index)
+    _launch("bitnet_add_rmsnorm_quant", index, stream, X.data_ptr(), R.data_ptr(), _addr(w), T, K, eps_norm, eps_act,
             H.data_ptr(), Xq.data_ptr(), absmax.data_ptr(), rinv.data_ptr())
     return H, Xq, absmax, rinv
 
@@ -530,15 +534,17 @@ def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumula
     Returns (dH, dw): dH of dR's (or dH's own) type, bf16 unless given; dw fp32."""
     torch = _torch()
     T, K = H.shape
-    assert _is(H, torch.bfloat16, (T, K), H) and H.is_cuda and _is(rinv, torch.float32, (T,), H)
-    assert dY.dtype in (torch.float32, torch.bfloat16) and _is(dY, dY.dtype, (T, K), H)
-    assert _is(w, torch.float32, (K,), H, optional=True)
+    f32, rows, index = torch.float32, (T, K), H.get_device()
+    assert H.is_cuda and _is(H, torch.bfloat16, rows, index) and _is(rinv, f32, (T,), index)
+    assert dY.dtype in (f32, torch.bfloat16) and _is(dY, dY.dtype, rows, index)
+    assert w is None or _is(w, f32, (K,), index)
     g = dH.dtype if dH is not None else dR.dtype if dR is not None else torch.bfloat16
     dH = _new((T, K), g, H, stream) if dH is None else dH
     dw = _new((K,), torch.float32, H, stream) if dw is None else dw
-    assert _is(dR, g, (T, K), H, optional=True) and _is(dH, g, (T, K), H) and _is(dw, torch.float32, (K,), H)
+    assert dR is None or _is(dR, g, rows, index)
+    assert _is(dH, g, rows, index) and _is(dw, f32, (K,), index)
     keep, ws_ptr, ws_bytes = _ws(ws, lambda: load().bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
-    _launch("bitnet_rmsnorm_grad", H, stream, dY.data_ptr(), _dtype_code(dY.dtype), H.data_ptr(), _addr(w),
+    _launch("bitnet_rmsnorm_grad", index, stream, dY.data_ptr(), _dtype_code(dY.dtype), H.data_ptr(), _addr(w),
             rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
             ws_ptr, ws_bytes)
     return dH, dw
@@ -612,15 +618,15 @@ def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interl
     if head_dim is None:
         head_dim = X.shape[1] // n_heads
     assert X.shape[1] >= n_heads * head_dim
-    assert _is(pos, torch.int32, (T,), X)
-    n_pos, half, two = table.shape
-    assert two == 2 and _is(table, torch.float32, (n_pos, half, 2), X)
+    index = X.get_device()
+    n_pos, half, _ = table.shape
+    assert _is(pos, torch.int32, (T,), index) and _is(table, torch.float32, (n_pos, half, 2), index)
     if Y is None:
         Y = _new((T, n_heads * head_dim), X.dtype, X, stream)
-    assert Y.dim() == 2 and Y.dtype == X.dtype and Y.get_device() == X.get_device() and Y.stride(1) == 1
+    assert Y.dim() == 2 and Y.dtype == X.dtype and Y.get_device() == index and Y.stride(1) == 1
     assert Y.shape[0] == T and Y.shape[1] >= n_heads * head_dim
     keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, X, stream)
-    _launch("bitnet_rope", X, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(), table.data_ptr(), n_pos,
+    _launch("bitnet_rope", index, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(), table.data_ptr(), n_pos,
             T, n_heads, head_dim, 2 * half, 1 if interleaved else 0, 1 if inverse else 0, Y.data_ptr(), _ld(Y), ws_ptr,
             ws_bytes)
     return Y
@@ -634,19 +640,21 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
     pages (int32 [sequences, most pages]).  table None: no rotation.  Returns Q (bf16 [T, heads * head_dim])."""
     torch = _torch()
     c = _cache_struct(K, V)
-    assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1 and QKV.get_device() == K.get_device()
+    assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1
+    index = K.get_device()
     T, width = QKV.shape
     heads = width // c.head_dim - 2 * c.n_kv_heads
     assert heads > 0 and width == (heads + 2 * c.n_kv_heads) * c.head_dim
-    assert _is(pos, torch.int32, (T,), QKV) and _is(seq, torch.int32, (T,), QKV, optional=True)
+    i32 = torch.int32
     n_seqs, max_pages = pages.shape
-    assert _is(pages, torch.int32, (n_seqs, max_pages), QKV)
+    assert QKV.get_device() == index and _is(pos, i32, (T,), index) and _is(pages, i32, (n_seqs, max_pages), index)
+    assert seq is None or _is(seq, i32, (T,), index)
     n_pos, half = (table.shape[0], table.shape[1]) if table is not None else (0, 0)
-    assert _is(table, torch.float32, (n_pos, half, 2), QKV, optional=True)
+    assert table is None or _is(table, torch.float32, (n_pos, half, 2), index)
     Q = _new((T, heads * c.head_dim), torch.bfloat16, QKV, stream) if Q is None else Q
-    assert _is(Q, torch.bfloat16, (T, heads * c.head_dim), QKV)
+    assert _is(Q, torch.bfloat16, (T, heads * c.head_dim), index)
     keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, QKV, stream)
-    _launch("bitnet_rope_append", QKV, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV), pos.data_ptr(), _addr(seq),
+    _launch("bitnet_rope_append", index, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV), pos.data_ptr(), _addr(seq),
             _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0, ctypes.byref(c), pages.data_ptr(), n_seqs,
             max_pages, Q.data_ptr(), ws_ptr, ws_bytes)
     return Q
@@ -660,19 +668,21 @@ def bitnet_paged_attn(Q, K, V, pages, lens, scale: float | None = None, O=None, 
     Returns O (bf16 unless o_dtype says fp32)."""
     torch = _torch()
     c = _cache_struct(K, V)
-    assert Q.dim() == 2 and Q.dtype == torch.bfloat16 and Q.stride(1) == 1 and Q.get_device() == K.get_device()
+    index = K.get_device()
+    assert Q.dim() == 2 and Q.dtype is torch.bfloat16 and Q.stride(1) == 1 and Q.get_device() == index
     n_seqs, width = Q.shape
     heads = width // c.head_dim
     assert heads > 0 and width == heads * c.head_dim
-    assert pages.dim() == 2 and _is(pages, torch.int32, (n_seqs, pages.shape[1]), Q) and _is(lens, torch.int32, (n_seqs,), Q)
+    max_pages = pages.shape[1]
+    assert _is(pages, torch.int32, (n_seqs, max_pages), index) and _is(lens, torch.int32, (n_seqs,), index)
     if O is None:
         O = _new((n_seqs, width), torch.bfloat16 if o_dtype is None else o_dtype, Q, stream)
-    assert O.shape == Q.shape and O.stride(1) == 1 and O.get_device() == Q.get_device() and (o_dtype is None or O.dtype == o_dtype)
-    assert _is(lse, torch.float32, (n_seqs, heads), Q, optional=True)
+    assert O.shape == Q.shape and O.stride(1) == 1 and O.get_device() == index and (o_dtype is None or O.dtype == o_dtype)
+    assert lse is None or _is(lse, torch.float32, (n_seqs, heads), index)
     keep, ws_ptr, ws_bytes = _ws(
         ws, lambda: load().bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream)
-    _launch("bitnet_paged_attn", Q, stream, Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(),
-            pages.shape[1], lens.data_ptr(), c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(),
+    _launch("bitnet_paged_attn", index, stream, Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(),
+            max_pages, lens.data_ptr(), c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(),
             _dtype_code(O.dtype), _ld(O), _addr(lse), ws_ptr, ws_bytes)
     return O
 
