@@ -676,27 +676,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     cp_wait<0>();
 }
 
-// Joins the partials of the heads that more than one CTA of the first launch worked on: CTA (query head, sequence).
-// A warp takes every fourth partial, 32 of them at a time: lane j holds the j-th one's maximum and sum.
+// Joins the partials of the heads that more than one CTA of the first launch worked on.  CTA (i, h) joins query head h
+// of the virtual head that CTA i of the first launch began and did not finish.  It finds that out before it waits for
+// the first launch: the lengths were complete before that one's CTAs let this launch begin.  A warp takes every fourth
+// partial, 32 of them at a time: lane j holds the j-th one's maximum and sum.
 __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParams p) {
-    __shared__ int64_t s_warp[2 * kWarps];
+    __shared__ int64_t s_scan[2 * kWarps];
+    __shared__ int s_at;
     __shared__ float s_top[kWarps], s_sum[kWarps];
     __shared__ float4 s_o[kWarps][64];
+    int64_t first = 0;
+    const int64_t units = sum_units(p, 0, &first, s_scan);
+    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);
+    const int i0 = blockIdx.x, h = blockIdx.y;
+    bool mine = i0 + 1 < ctas;
+    int b = 0, head = 0, i1 = 0;
+    if (mine) {
+        const int64_t u = range_start(units, ctas, i0 + 1);   // the first unit behind CTA i0's range
+        b = find_seq(p, u, &first, s_scan, &s_at);
+        const int64_t n_units = (length_of(p, b) + p.unit - 1) / p.unit;
+        const int vh = static_cast<int>((u - first) / n_units), sub = vh % p.vper;
+        first += vh * n_units;
+        head = vh / p.vper * p.group + sub * p.per_vhead + h;
+        mine = u > first && range_start(units, ctas, i0) <= first && h < p.group - sub * p.per_vhead;
+        i1 = static_cast<int>(((first + n_units) * ctas - 1) / units);   // the CTA of its last unit: the largest i with range_start(i) below its end
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x / p.n_heads, head = blockIdx.x % p.n_heads;
-    const int64_t n_units = (length_of(p, b) + p.unit - 1) / p.unit;
-    if (n_units < 2) return;
-    const int kvh = head / p.group, in_group = head % p.group;
-    const int vh = kvh * p.vper + in_group / p.per_vhead, h = in_group % p.per_vhead;
-    int64_t first;
-    const int64_t units = sum_units(p, b, &first, s_warp);
-    first += vh * n_units;
-    const int64_t end = first + n_units;
-    // CTA of unit u: the largest i with range_start(i) <= u
-    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);
-    const int i0 = static_cast<int>(((first + 1) * ctas - 1) / units), i1 = static_cast<int>((end * ctas - 1) / units);
-    if (i0 == i1) return;
+    if (!mine) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t size = part_floats(p.per_vhead, p.head_dim);
     const int row = part_row(p.head_dim);
@@ -705,10 +712,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
     float top = -INFINITY, sum = 0.0f;
     float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int j0 = i0 + warp; j0 <= i1; j0 += kWarps * 32) {
-        const int mine = j0 + kWarps * lane;
+        const int ij = j0 + kWarps * lane;
         float mi = -INFINITY, li = 0.0f;
-        if (mine <= i1) {
-            const float *ml = partial(mine) + p.per_vhead * row + 2 * h;
+        if (ij <= i1) {
+            const float *ml = partial(ij) + p.per_vhead * row + 2 * h;
             mi = ml[0];
             li = ml[1];
         }
@@ -811,8 +818,8 @@ cudaError_t go(AttnParams p, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, KT, ST, FULL>, p);
     if (e != cudaSuccess) return e;
-    if ((p.max_pages << p.page_shift) <= p.unit) return cudaSuccess;   // one unit per head at most: nothing to join
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.n_seqs) * p.n_heads));
+    if (p.grid < 2 || (p.max_pages << p.page_shift) <= p.unit) return cudaSuccess;   // one CTA, or one unit per head at most: nothing to join
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(p.per_vhead));
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_paged_attn_join, p);
 }
