@@ -181,8 +181,59 @@ __device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t 
     return p.n_seqs;   // not reached for u below the total
 }
 
+// a / b of non-negative values; 32-bit where they fit (a 64-bit division takes a few hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // first unit of CTA i's range
-__device__ __forceinline__ int64_t range_start(int64_t units, int ctas, int i) { return units * i / ctas; }
+__device__ __forceinline__ int64_t range_start(int64_t units, int ctas, int i) { return quotient(units * i, ctas); }
+
+// Where CTA range `index` begins: *units in all, *ctas that work, and for index < *ctas the sequence and the units
+// before it.  Up to 128 sequences take one look at the lengths, more of them two passes.
+struct Shares {
+    int64_t units, start, first;   // units in all, first unit of the range, units before sequence b
+    int ctas, b;
+};
+__device__ Shares find_range(const AttnParams &p, int index, int64_t *s_scan, int *s_at) {
+    Shares r;
+    if (p.n_seqs > kWarps * 32) {
+        r.units = sum_units(p, 0, &r.first, s_scan);
+        r.ctas = static_cast<int>(r.units < p.grid ? r.units : p.grid);
+        if (index >= r.ctas) return r;
+        r.start = range_start(r.units, r.ctas, index);
+        r.b = find_seq(p, r.start, &r.first, s_scan, s_at);
+        return r;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t mine = static_cast<int>(threadIdx.x) < p.n_seqs ? units_of(p, threadIdx.x) : 0;
+    int64_t s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += x;
+    }
+    if (lane == 31) s_scan[warp] = s;
+    __syncthreads();
+    r.units = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) s += s_scan[i];
+        r.units += s_scan[i];
+    }
+    r.ctas = static_cast<int>(r.units < p.grid ? r.units : p.grid);
+    if (index >= r.ctas) return r;   // the same for the whole CTA
+    r.start = range_start(r.units, r.ctas, index);
+    if (s - mine <= r.start && r.start < s) {
+        s_scan[kWarps] = s - mine;
+        *s_at = threadIdx.x;
+    }
+    __syncthreads();
+    r.first = s_scan[kWarps];
+    r.b = *s_at;
+    return r;
+}
 
 // floats of one partial: per query head o in a row of head_dim rounded up to 4, then m and the sum of each
 __host__ __device__ __forceinline__ int part_row(int head_dim) { return (head_dim + 3) & ~3; }
@@ -253,20 +304,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 p.lse[static_cast<int64_t>(b) * p.n_heads + i] = -INFINITY;
     }
 
-    int64_t first = 0;
-    const int64_t units = sum_units(p, 0, &first, sh.scan);
-    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);   // every one of them gets a unit
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
-    const int64_t lo = range_start(units, ctas, blockIdx.x);
-    const int todo = static_cast<int>(range_start(units, ctas, blockIdx.x + 1) - lo);
+    const Shares share = find_range(p, blockIdx.x, sh.scan, &sh.at);
+    if (static_cast<int>(blockIdx.x) >= share.ctas) return;   // every CTA that works gets a unit
+    const int todo = static_cast<int>(range_start(share.units, share.ctas, blockIdx.x + 1) - share.start);
     Walker at;   // the unit being worked on
-    at.b = find_seq(p, lo, &first, sh.scan, &sh.at);
+    at.b = share.b;
     at.len = length_of(p, at.b);
     at.n = (at.len + kUnit - 1) / kUnit;
-    const int vhead = static_cast<int>((lo - first) / at.n);
+    const int vhead = static_cast<int>(quotient(share.start - share.first, at.n));
     at.kv = vhead / p.vper;
     at.sub = vhead % p.vper;
-    at.j = static_cast<int>((lo - first) % at.n);
+    at.j = static_cast<int>(share.start - share.first - static_cast<int64_t>(vhead) * at.n);
 
     // A piece in the ring: rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take
     // a segment, 16 bytes each.  The 16-byte chunk k of a segment lies at k ^ 4 (r & 1) for K, k ^ (r & 6) for V, so
@@ -685,21 +733,20 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
     __shared__ int s_at;
     __shared__ float s_top[kWarps], s_sum[kWarps];
     __shared__ float4 s_o[kWarps][64];
-    int64_t first = 0;
-    const int64_t units = sum_units(p, 0, &first, s_scan);
-    const int ctas = static_cast<int>(units < p.grid ? units : p.grid);
     const int i0 = blockIdx.x, h = blockIdx.y;
-    bool mine = i0 + 1 < ctas;
+    const Shares next = find_range(p, i0 + 1, s_scan, &s_at);   // behind CTA i0's range
+    bool mine = i0 + 1 < next.ctas, late = false;
     int b = 0, head = 0, i1 = 0;
     if (mine) {
-        const int64_t u = range_start(units, ctas, i0 + 1);   // the first unit behind CTA i0's range
-        b = find_seq(p, u, &first, s_scan, &s_at);
+        b = next.b;
         const int64_t n_units = (length_of(p, b) + p.unit - 1) / p.unit;
-        const int vh = static_cast<int>((u - first) / n_units), sub = vh % p.vper;
-        first += vh * n_units;
+        const int vh = static_cast<int>(quotient(next.start - next.first, n_units)), sub = vh % p.vper;
+        const int64_t first = next.first + vh * n_units, begin = range_start(next.units, next.ctas, i0);
         head = vh / p.vper * p.group + sub * p.per_vhead + h;
-        mine = u > first && range_start(units, ctas, i0) <= first && h < p.group - sub * p.per_vhead;
-        i1 = static_cast<int>(((first + n_units) * ctas - 1) / units);   // the CTA of its last unit: the largest i with range_start(i) below its end
+        mine = next.start > first && begin <= first && h < p.group - sub * p.per_vhead;
+        late = begin < first;   // the head is not the first of i0's range: its partial is in slot 1
+        // the CTA of the head's last unit: the largest i with range_start(i) below its end
+        i1 = static_cast<int>(quotient((first + n_units) * next.ctas - 1, next.units));
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -707,8 +754,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t size = part_floats(p.per_vhead, p.head_dim);
     const int row = part_row(p.head_dim);
-    // partial i: in slot 0 when the range begins inside the head's keys, else (only i0 can) in slot 1
-    auto partial = [&](int i) { return p.part + (2 * static_cast<int64_t>(i) + (i == i0 && range_start(units, ctas, i) < first ? 1 : 0)) * size; };
+    auto partial = [&](int i) { return p.part + (2 * static_cast<int64_t>(i) + (i == i0 && late ? 1 : 0)) * size; };
     float top = -INFINITY, sum = 0.0f;
     float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int j0 = i0 + warp; j0 <= i1; j0 += kWarps * 32) {
@@ -734,18 +780,23 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
             o[c].x *= f; o[c].y *= f; o[c].z *= f; o[c].w *= f;
         }
         const int n = min(32, (i1 - j0) / kWarps + 1);
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) {
-            const float fj = __shfl_sync(0xffffffffu, fi, j);
-            const float4 *src = reinterpret_cast<const float4 *>(partial(j0 + kWarps * j) + h * row);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (4 * (lane + 32 * c) < row) {
-                    const float4 v = src[lane + 32 * c];
-                    o[c].x = fmaf(v.x, fj, o[c].x);
-                    o[c].y = fmaf(v.y, fj, o[c].y);
-                    o[c].z = fmaf(v.z, fj, o[c].z);
-                    o[c].w = fmaf(v.w, fj, o[c].w);
+        for (int c = 0; c < 2; ++c) {
+            if (c == 1 && row <= 128) break;
+            const int at = 4 * (lane + 32 * c) < row ? 4 * (lane + 32 * c) : 0;   // lanes without features repeat the first
+            for (int j = 0; j < n; j += 8) {
+                // eight loads with no condition, so that they are in flight together; those behind the last one count 0
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = *reinterpret_cast<const float4 *>(partial(j0 + kWarps * min(j + k, n - 1)) + h * row + at);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float fj = j + k < n ? __shfl_sync(0xffffffffu, fi, j + k) : 0.0f;
+                    o[c].x = fmaf(v[k].x, fj, o[c].x);
+                    o[c].y = fmaf(v[k].y, fj, o[c].y);
+                    o[c].z = fmaf(v[k].z, fj, o[c].z);
+                    o[c].w = fmaf(v[k].w, fj, o[c].w);
                 }
             }
         }
