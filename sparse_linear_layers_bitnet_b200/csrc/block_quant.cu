@@ -415,16 +415,16 @@ __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
 // written to H once (H may be X or R: a thread writes only what it alone has
 // read).  Per element 2 + 2 bytes in and 2 + 1 out.
 template <int CPT, bool ADD>
-__global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *X, const uint4 *R, uint4 *H,
+__global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const uint4 *R, uint4 *H,
                                                          const float4 *__restrict__ w,
                                                          int K, double inv_k, float eps_n, float eps_a,
                                                          int8_t *__restrict__ Xq, float *__restrict__ amax,
                                                          float *__restrict__ rinv) {
     __shared__ unsigned long long s_bins[kSqBins];
-    __shared__ unsigned long long s_lo[8], s_hi[8];
+    __shared__ unsigned long long s_lo[16], s_hi[16];
     __shared__ uint32_t s_limb[kSqLimbs];
-    __shared__ float s_red[8];
-    __shared__ double s_sq[8];
+    __shared__ float s_red[16];
+    __shared__ double s_sq[16];
     __shared__ float s_r;
     const int64_t t = blockIdx.x;
     const int nchunk = K >> 3;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(256) k_rmsnorm_quant_rc(const uint4 *X, const 
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // S by fp64 fused multiply-adds.  At most 64 of them per thread, 5 steps in a warp and 8 over the warps: the sum is
+    // S by fp64 fused multiply-adds.  At most 64 of them per thread, 5 steps in a warp and 16 over the warps: the sum is
     // within 2^-46 of the exact one, and so are 1/K and the product.  Where everything within 2^-44 of the quotient
     // rounds to the same fp32 (all but one row in 2^19), that is ms; else, and for tiny rows (zeros and subnormals are
     // taken as about 2^-127 here), the exact sum below decides.
@@ -693,7 +693,7 @@ static int pick_cpt(int64_t nchunk, const int *list, int n, int max_threads, int
     return 0;
 }
 
-constexpr int kRmsCpt[] = {1, 2, 3, 4, 6, 8};   // larger CPT spills registers
+constexpr int kRmsCpt[] = {1, 2, 3, 4, 6, 8};   // larger CPT spills registers; 8 of 512 threads hold rows of 32768
 constexpr int kSwiCpt[] = {1, 2, 3, 4, 6, 8};
 
 template <int CPT, bool ADD>
@@ -713,8 +713,14 @@ static cudaError_t rms_launch(const void *X, const void *R, void *H, const float
     int threads = 0;
     int cpt = 0;
     if (!(reinterpret_cast<uintptr_t>(w) & 15u)) {
-        cpt = pick_cpt(K / 8, kRmsCpt, 6, 128, &threads);
-        if (cpt == 0) cpt = pick_cpt(K / 8, kRmsCpt, 6, 256, &threads);
+        // What a thread does whatever its share (both reductions, the root and two divisions) costs about as much as two
+        // chunks, so many rows take few threads each; where all rows are in flight at once a row's latency counts and
+        // it takes more.  Up to four chunks a thread while 512 threads do (six spill).  Measured (us, up to 128 / 256 /
+        // 512 threads): 1 x 2560 2.8 / 2.5 / 2.3, 2048 x 3200 14.5 / 12.9 / 15.6, 16381 x 4096 85.9 / 91.2 / 116,
+        // 6000 x 8640 (six chunks with 128 and 256) 98.6 / 98.6 / 79.6.
+        int most = T <= 2 * num_sms() ? 512 : T <= 16 * num_sms() ? 256 : 128;
+        while (most < 512 && K / 8 > 4 * most) most *= 2;
+        cpt = pick_cpt(K / 8, kRmsCpt, 6, most, &threads);
     }
     if (cpt == 0) {   // rows beyond the register cache, or a weight vector without 16-byte alignment
         cudaLaunchConfig_t cfg = bq_config(T, kBqThreads, 0, s, attr);

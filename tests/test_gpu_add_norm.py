@@ -61,7 +61,8 @@ def _rows(T, K, seed):
 
 
 @pytest.mark.parametrize("T,K,weighted", [(1, 8, False), (1, 2560, True), (7, 264, True), (33, 3200, True), (5, 4096, False),
-                                          (6, 8640, True), (5, 16384, True), (5, 20000, True), (5, 65536, False)])
+                                          (6, 8640, True), (5, 16384, True), (5, 20000, True), (5, 32768, True),
+                                          (5, 40000, True), (5, 65536, False), (300, 3200, True), (2400, 264, False)])
 def test_add_rmsnorm_quant_matches_the_oracle(bn, T, K, weighted):
     Xf, Rf = _rows(T, K, T * 7 + K)
     Xd, X = bf16_dev(Xf)
@@ -80,7 +81,7 @@ def test_add_rmsnorm_quant_matches_the_oracle(bn, T, K, weighted):
     assert np.array_equal(Xq.cpu().numpy(), q)
 
 
-@pytest.mark.parametrize("K", [512, 3200, 24576])
+@pytest.mark.parametrize("K", [512, 3200, 24576, 40960])
 @pytest.mark.parametrize("into", ["X", "R"])
 def test_the_sum_may_go_into_an_input(bn, K, into):
     Xd, _ = bf16_dev(synth.activations(9, K, seed=K))
@@ -94,7 +95,7 @@ def test_the_sum_may_go_into_an_input(bn, K, into):
     assert torch.equal(Rd if into == "X" else Xd, other)
 
 
-@pytest.mark.parametrize("K", [2560, 16392])
+@pytest.mark.parametrize("K", [2560, 32776])
 def test_a_weight_off_16_bytes_gives_the_same(bn, K):
     Xd, _ = bf16_dev(synth.activations(4, K, seed=1))
     Rd, _ = bf16_dev(synth.activations(4, K, seed=2))
