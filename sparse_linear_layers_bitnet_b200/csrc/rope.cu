@@ -73,6 +73,41 @@ template <typename TI, int VEC, bool INTERLEAVED>
 constexpr int kHeads = 64 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) < 4
                            ? 64 / (kVectors<VEC, INTERLEAVED> * VEC * static_cast<int>(sizeof(TI))) : 4;
 
+// two neighbouring features of a vector, rounded together
+template <int VEC>
+__device__ __forceinline__ void put2(Vec<float, VEC> &w, int i, float x, float y) {
+    w.v[i] = x;
+    w.v[i + 1] = y;
+}
+template <int VEC>
+__device__ __forceinline__ void put2(Vec<__nv_bfloat16, VEC> &w, int i, float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    w.v[i] = h.x;
+    w.v[i + 1] = h.y;
+}
+
+// Turns the pairs of one place: the halves of pair i lie in the two vectors (halves layout) or side by side
+// (interleaved).  Scalar operations: the paired ones (f32x2) are joined into a fused multiply-add by the compiler, in
+// PTX with .rn too, which rounds once less.
+template <typename TI, typename TO, int VEC, bool INTERLEAVED, int NV, int PAIRS>
+__device__ __forceinline__ void turn_place(const Vec<TI, VEC> (&v)[NV], Vec<TO, VEC> (&w)[NV], const float (&c)[PAIRS], const float (&s)[PAIRS]) {
+    float x[2 * PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
+        const float a = widen(v[ea / VEC].v[ea % VEC]), b = widen(v[eb / VEC].v[eb % VEC]);
+        x[ea] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+        x[eb] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+    }
+    if constexpr (VEC == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) w[i].v[0] = narrow<TO>(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV * VEC; i += 2) put2(w[i / VEC], i % VEC, x[i], x[i + 1]);
+    }
+}
+
 template <typename TI, typename TO, int VEC, bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(256, 4) k_rope(const RopeParams p) {
     constexpr int NV = kVectors<VEC, INTERLEAVED>, HEADS = kHeads<TI, VEC, INTERLEAVED>;
@@ -171,16 +206,7 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeParams p) {
         }
         VO u[NV];
         if (turns && !(APPEND && h >= p.heads + p.kv_heads)) {
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) {
-                // pair i: its halves lie in the two vectors (halves layout) or side by side (interleaved).  Scalar
-                // operations: the paired ones (f32x2) are joined into a fused multiply-add by the compiler, in PTX
-                // with .rn too, which rounds once less.
-                const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
-                const float fa = widen(v[j][ea / VEC].v[ea % VEC]), fb = widen(v[j][eb / VEC].v[eb % VEC]);
-                u[ea / VEC].v[ea % VEC] = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
-                u[eb / VEC].v[eb % VEC] = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
-            }
+            turn_place<TI, TO, VEC, INTERLEAVED>(v[j], u, c, s);
         } else {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
@@ -349,13 +375,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32) k_rope_rows(const RopePa
                     v[0] = *reinterpret_cast<const VI *>(src + off[0]);
                     if (has1) v[NV - 1] = *reinterpret_cast<const VI *>(src + off[1]);
                     if (turn) {
-#pragma unroll
-                        for (int i = 0; i < PAIRS; ++i) {
-                            const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : i + VEC;
-                            const float fa = widen(v[ea / VEC].v[ea % VEC]), fb = widen(v[eb / VEC].v[eb % VEC]);
-                            w[ea / VEC].v[ea % VEC] = narrow<TO>(__fsub_rn(__fmul_rn(fa, c[i]), __fmul_rn(fb, s[i])));
-                            w[eb / VEC].v[eb % VEC] = narrow<TO>(__fadd_rn(__fmul_rn(fb, c[i]), __fmul_rn(fa, s[i])));
-                        }
+                        turn_place<TI, TO, VEC, INTERLEAVED>(v, w, c, s);
                     } else {
 #pragma unroll
                         for (int i = 0; i < NV; ++i)
