@@ -346,7 +346,8 @@ bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float
     if (!X || !R || !H || !Xq || !absmax) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: null pointer");
     if (!aligned(X, 16) || !aligned(R, 16) || !aligned(H, 16) || !aligned(Xq, 16))
         return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: X, R, H and Xq must be 16-byte aligned");
-    if (w && !aligned(w, 4)) return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: w must be 4-byte aligned");
+    if (!aligned(w, 4) || !aligned(absmax, 4) || !aligned(rinv, 4))
+        return fail(BITNET_ERR_INVALID_ARG, "add_rmsnorm_quant: w, absmax and rinv must be 4-byte aligned");
     if (T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "add_rmsnorm_quant: T too large");
     const size_t bytes = static_cast<size_t>(T) * static_cast<size_t>(K) * 2;
     if ((H != X && overlaps(H, bytes, X, bytes)) || (H != R && overlaps(H, bytes, R, bytes)) ||
@@ -373,8 +374,8 @@ bitnet_status bitnet_rmsnorm_grad(const void *dY, bitnet_dtype dy_dtype, const v
         return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(K) * 4, s), "rmsnorm_grad");
     }
     if (!dY || !H || !rinv || !dH) return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: null pointer");
-    if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(dH, 16) || !aligned(dR, 16) || !aligned(w, 16))
-        return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: dY, H, w, dR and dH must be 16-byte aligned");
+    if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(dH, 16) || !aligned(dR, 16) || !aligned(w, 16) || !aligned(rinv, 4))
+        return fail(BITNET_ERR_INVALID_ARG, "rmsnorm_grad: dY, H, w, dR and dH must be 16-byte, rinv 4-byte aligned");
     if (T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "rmsnorm_grad: T too large");
     if (dw) {
         if (!ws) return fail(BITNET_ERR_WORKSPACE, "rmsnorm_grad: dw needs a workspace");
@@ -479,6 +480,7 @@ bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld
     bitnet::KvCacheHost c;
     bitnet_status st = kv_cache_check("rope_append", cache, &c);
     if (st != BITNET_OK) return st;
+    if (c.k == c.v) return fail(BITNET_ERR_INVALID_ARG, "rope_append: keys and values would be written to the same rows");
     if (T < 0 || n_heads < 1 || n_seqs < 0 || max_pages < 1) return fail(BITNET_ERR_INVALID_ARG, "rope_append: bad sizes");
     if (n_heads > 65535 || T > 2147483647LL) return fail(BITNET_ERR_UNSUPPORTED, "rope_append: T or n_heads too large");
     if (ld < (n_heads + 2 * static_cast<int64_t>(c.n_kv_heads)) * c.head_dim)

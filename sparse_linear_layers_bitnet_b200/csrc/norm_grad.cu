@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(CPT == 2 ? 576 : 512) k_rmsnorm_grad(const TY 
     Raw8<__nv_bfloat16> nh[CPT];
     Raw8<TG> nr[CPT];
     float next_r = 0.0f;
-    auto fetch = [&](int t) {
+    // rows are counted without a sign: T < 2^31 and a step further does not overflow
+    const unsigned rows = T;
+    auto fetch = [&](unsigned t) {
         const int64_t base = static_cast<int64_t>(t) * K;
         next_r = __ldg(rinv + t);
 #pragma unroll
@@ -111,9 +113,9 @@ __global__ void __launch_bounds__(CPT == 2 ? 576 : 512) k_rmsnorm_grad(const TY 
             }
         }
     };
-    if (kAhead && static_cast<int>(blockIdx.x) < T) fetch(blockIdx.x);
+    if (kAhead && blockIdx.x < rows) fetch(blockIdx.x);
     int flip = 0;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    for (unsigned t = blockIdx.x; t < rows; t += gridDim.x) {
         const int64_t base = static_cast<int64_t>(t) * K;
         if (!kAhead) fetch(t);
         const float r = next_r;
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(CPT == 2 ? 576 : 512) k_rmsnorm_grad(const TY 
                 for (int i = 0; i < 8; ++i) e[j][i] = u[j][i] = 0.0f;
             }
         }
-        if (kAhead && t + static_cast<int>(gridDim.x) < T) fetch(t + gridDim.x);
+        if (kAhead && t + gridDim.x < rows) fetch(t + gridDim.x);
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(256) k_rmsnorm_dw(const TY *__restrict__ dY, c
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
     if (c >= (K >> 3)) return;
     float dw[8] = {};
-    for (int t = blockIdx.y; t < T; t += gridDim.y) {
+    for (unsigned t = blockIdx.y; t < static_cast<unsigned>(T); t += gridDim.y) {
         const int64_t base = static_cast<int64_t>(t) * K;
         const float r = __ldg(rinv + t);
         float e[8], u[8];

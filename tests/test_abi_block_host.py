@@ -34,7 +34,8 @@ def test_add_rmsnorm_quant_refusals(lib):
         assert call(f, ok, **{name: None}) == INVALID, name
     for name in ("X", "R", "H", "Xq"):
         assert call(f, ok, **{name: ok[name] + 8}) == INVALID, name
-    assert call(f, ok, w=at(3, 2)) == INVALID
+    for name in ("w", "absmax", "rinv"):
+        assert call(f, ok, **{name: ok[name] + 2}) == INVALID, name
     for K in (0, 4, 65544):
         assert call(f, ok, K=K) == INVALID
     assert call(f, ok, T=-1) == INVALID
@@ -58,6 +59,8 @@ def test_rmsnorm_grad_refusals(lib):
         assert call(f, ok, **{name: None}) == INVALID, name
     for name in ("dY", "H", "w", "dR", "dH", "ws"):
         assert call(f, ok, **{name: ok[name] + 8}) == INVALID, name
+    for name in ("rinv", "dw"):
+        assert call(f, ok, **{name: ok[name] + 2}) == INVALID, name
     for name in ("dy_dtype", "g_dtype"):
         assert call(f, ok, **{name: 2}) == INVALID
     for K in (0, 12, 65544):
@@ -118,6 +121,7 @@ def test_rope_append_refusals(lib):
     for name, bad in (("dtype", 3), ("ld", 3839), ("n_pos", 0), ("T", -1), ("n_heads", 0), ("n_seqs", -1), ("max_pages", 0),
                       ("rot_dim", 130), ("rot_dim", 63), ("layout", 2)):
         assert call(f, ok, **{name: bad}) == INVALID, name
+    assert call(f, ok, cache=cache(v=at(10))) == INVALID        # keys and values in one place
     assert call(f, ok, seq=None) == INVALID                     # four rows, two sequences
     assert call(f, ok, Q=at(1, 4096)) == INVALID
     assert call(f, ok, T=1 << 31) == UNSUPPORTED
