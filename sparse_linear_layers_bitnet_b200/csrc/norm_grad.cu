@@ -77,8 +77,8 @@ __device__ __forceinline__ void store8(float *row, int c, const float *f) {
 
 // CPT chunks of 8 columns per thread; the row's K / 8 chunks lie at threadIdx.x
 // + j blockDim.x.  dwp: [gridDim.x, K] partial dw rows, or NULL.
-template <typename TY, typename TG, int CPT>
-__global__ void __launch_bounds__(CPT == 2 ? 576 : 512) k_rmsnorm_grad(const TY *__restrict__ dY, const __nv_bfloat16 *__restrict__ H,
+template <typename TY, typename TG, int CPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_rmsnorm_grad(const TY *__restrict__ dY, const __nv_bfloat16 *__restrict__ H,
                                                       const float *__restrict__ w, const float *__restrict__ rinv,
                                                       const TG *dR, TG *dH, float *__restrict__ dwp, int T, int K) {
     __shared__ float s_red[2][32];
@@ -294,18 +294,18 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
 
 // Chunks per thread and threads of the row kernel (0 chunks: rows too long for it).
 int chunks_per_thread(int64_t nchunk, int *threads) {
-    const int cpt = nchunk <= 512 ? 1 : nchunk <= 1152 ? 2 : nchunk <= 1536 ? 3 : 0;
+    const int cpt = nchunk <= 1024 ? 1 : nchunk <= 1152 ? 2 : nchunk <= 1536 ? 3 : 0;
     *threads = cpt ? static_cast<int>((nchunk + cpt - 1) / cpt + 31) / 32 * 32 : 512;
     return cpt;
 }
 
-// CTAs of the row kernel, each with a partial dw row: about 1024 threads per SM, two CTAs at least and eight at most
-// (more of them cost more in partial rows than they hide: 4 instead of 2 per SM at K = 4096 53.1 against 48.8 us).
+// CTAs of the row kernel, each with a partial dw row: as many as fit an SM's registers with about 1024 threads, eight at
+// most (more of them cost more in partial rows than they hide: 4 instead of 2 per SM at K = 4096 53.1 against 48.8 us).
 int partial_rows(int64_t T, int64_t K) {
     int threads;
-    chunks_per_thread(K / 8, &threads);
-    int per_sm = 1024 / threads;
-    per_sm = per_sm < 2 ? 2 : per_sm > 8 ? 8 : per_sm;
+    const int cpt = chunks_per_thread(K / 8, &threads);
+    int per_sm = cpt > 1 ? 1 : 1024 / threads;
+    per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
     const int64_t most = static_cast<int64_t>(per_sm) * num_sms();
     return static_cast<int>(T < most ? T : most);
 }
@@ -316,9 +316,11 @@ cudaError_t grad_launch(const TY *dY, const __nv_bfloat16 *H, const float *w, co
     const int nchunk = K / 8, rows = partial_rows(T, K);
     int threads;
     switch (chunks_per_thread(nchunk, &threads)) {
-        case 1: return launch_pdl(k_rmsnorm_grad<TY, TG, 1>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
-        case 2: return launch_pdl(k_rmsnorm_grad<TY, TG, 2>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
-        case 3: return launch_pdl(k_rmsnorm_grad<TY, TG, 3>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
+        case 1:   // 65536 / 512 registers a thread measured better than 65536 / 1024 wherever they do: 47.2 / 49.6 us at 8191 x 4096
+            if (threads <= 512) return launch_pdl(k_rmsnorm_grad<TY, TG, 1, 512>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
+            return launch_pdl(k_rmsnorm_grad<TY, TG, 1, 1024>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
+        case 2: return launch_pdl(k_rmsnorm_grad<TY, TG, 2, 576>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
+        case 3: return launch_pdl(k_rmsnorm_grad<TY, TG, 3, 512>, dim3(rows), dim3(threads), s, dY, H, w, rinv, dR, dH, dwp, T, K);
     }
     cudaError_t e = launch_pdl(k_rmsnorm_grad_long<TY, TG>, dim3(T), dim3(512), s, dY, H, w, rinv, dR, dH, K);
     if (e != cudaSuccess || !dwp) return e;
