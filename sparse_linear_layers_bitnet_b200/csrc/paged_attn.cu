@@ -57,7 +57,7 @@ struct AttnParams {
     uint32_t *status;
     int unit;                         // keys per unit
     int shift;                        // rows of the ring have a chunk to spare, and pages hold whole sectors (see the kernel)
-    int q_vec;                        // Q's rows and heads lie on 16 bytes
+    int q_vec;                        // bytes on which Q's rows and heads lie: 16, 8 or 2
     int grid;                         // CTAs of the first launch (those behind the number of units stay idle)
 };
 
@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     // A piece in the ring: rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take
     // a segment, 16 bytes each.  The 16-byte chunk k of a segment lies at k ^ 4 (r & 1) for K, k ^ (r & 6) for V, so
     // that the eight lanes of a read phase (below) meet eight different chunks.  Where rows may start in the middle of
-    // a 32-byte sector (p.shift: the ring's rows have a chunk to spare then), those rows lie one chunk further on, so
-    // that sectors stay whole; which ones depends on the head (`odd`) and, for strides of an odd number of chunks, on
-    // the row.
+    // a 32-byte sector (p.shift: the ring's rows have a chunk to spare then), those rows are copied from 16 bytes before
+    // their start, a place that is not read, and so lie one chunk further on: sectors stay whole.  Which rows depends on
+    // the head, and for strides of an odd number of chunks on the row.
     const uint32_t ring = smem_u32(smem) + warp * (ST * kPiece);
     const int cq = lane >> 3, cj = lane & 7;   // copies: row of four, chunk
     const uint32_t turn = FULL ? 0u : static_cast<uint32_t>(p.shift) & static_cast<uint32_t>(p.row_stride >> 3);   // odd rows differ from even ones
@@ -330,9 +330,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     const int row_mask = (1 << p.page_shift) - 1;
     const int64_t row4 = 4 * p.row_stride, lane_at = cq * p.row_stride + 8 * cj;
     const bool one_page = ((KT - 1) >> p.page_shift) == 0;   // a tile lies in one page
-    bool have[DB];   // this lane's chunk of each segment holds features
+    // segments of which this lane's chunk holds features, in a row that lies where it should and in one a chunk further on
+    uint32_t have0 = 0, have1 = 0;
 #pragma unroll
-    for (int d = 0; d < DB; ++d) have[d] = FULL || 8 * d + cj <= last_piece;
+    for (int d = 0; d < DB; ++d) {
+        have0 |= 8 * d + cj <= last_piece ? 1u << d : 0u;
+        have1 |= 8 * d + cj >= 1 && 8 * d + cj - 1 <= last_piece ? 1u << d : 0u;
+    }
     // words of K's pieces 4 (last_piece / 4) + t that hold features: what lies behind head_dim may be anything
     uint32_t keep[4];
 #pragma unroll
@@ -366,10 +370,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     };
     // copies one piece: rows 4 h + cq of the groups
     auto copy = [&](const __nv_bfloat16 *head, bool values, int key, uint32_t ok) {
-        const __nv_bfloat16 *from = head + lane_at;
-        const uint32_t on = FULL ? 0u : (odd_of(head) ^ (cq & turn)) & 1u;
-        const uint32_t chunk = (cj + on) & 7, dst = ring + slot * kPiece + cq * DB * 128 + ((cj + on) >> 3) * 128;
-        const uint32_t to0 = dst + ((chunk ^ (values ? cq & 2 : 4 * (cq & 1))) << 4);
+        const uint32_t on = FULL ? 0u : (odd_of(head) ^ (cq & turn)) & 1u, have = on ? have1 : have0;
+        const __nv_bfloat16 *from = head + lane_at - (FULL ? 0 : 8 * static_cast<int>(on));
+        const uint32_t to0 = ring + slot * kPiece + cq * DB * 128 + ((cj ^ (values ? cq & 2 : 4 * (cq & 1))) << 4);
         const uint32_t to1 = values ? to0 ^ 64u : to0;   // rows 4 to 7 of a group
         if (plain) {   // the common case without a test per row
 #pragma unroll
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 const __nv_bfloat16 *src = from + off[h >> 1] + (h & 1 ? row4 : 0);
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    if (FULL || have[d]) cp16(to + d * 128, src + 64 * d);
+                    if (FULL || (have >> d & 1u)) cp16(to + d * 128, src + 64 * d);
             }
         } else {
 #pragma unroll
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 const bool in = (ok >> (h >> 1) & 1u) && key + 4 * h + cq < ahead.len;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    if (FULL || have[d]) cp16_or_zero(to + d * 128, in ? src + 64 * d : p.k, in);
+                    if (FULL || (have >> d & 1u)) cp16_or_zero(to + d * 128, in ? src + 64 * d : p.k, in);
             }
         }
     };
@@ -450,11 +453,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + w.b * p.ldq +
                                       static_cast<int64_t>(head0 + h) * p.head_dim + f;
                 if (h < heads) {
-                    if (p.q_vec) {
+                    if (p.q_vec == 16) {
                         if (FULL || f < p.head_dim) {
                             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
                             x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
                         }
+                    } else if (p.q_vec == 8) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (f + 4 * e < p.head_dim) {
+                                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + e);
+                                x[2 * e] = v.x;
+                                x[2 * e + 1] = v.y;
+                            }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -911,7 +922,9 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
     p.o = O; p.o_bf16 = o_bf16 ? 1 : 0; p.ldo = ldo; p.lse = lse;
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
     p.status = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kStatusOffset);
-    p.q_vec = c.head_dim % 8 == 0 && ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(Q) & 15) == 0;
+    p.q_vec = c.head_dim % 8 == 0 && ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(Q) & 15) == 0   ? 16
+              : c.head_dim % 4 == 0 && ldq % 4 == 0 && (reinterpret_cast<uintptr_t>(Q) & 7) == 0 ? 8
+                                                                                                 : 2;
     // 32 keys at once and two to four CTAs per SM; at 256 features 16 keys, so that two CTAs fit
     if (c.head_dim <= 64) return by_heads<1, 32, 4>(p, s);
     if (c.head_dim <= 128) return by_heads<2, 32, 3>(p, s);
