@@ -1,5 +1,6 @@
 // Block epilogues fused into per-token int8 quantisation (sm_100a):
-// RMSNorm -> quant and SwiGLU -> quant.
+// RMSNorm -> quant (with or without a residual addition before it) and
+// SwiGLU -> quant.
 //
 // "BitNet b1.58: Ternary Weights for 1.58-bit LLMs", "What this paper
 // explains" item 3: the Transformer stack around BitLinear is LLaMA-alike
@@ -20,8 +21,11 @@
 // as in bitnet_quant_act.  Every step is a single IEEE operation in a fixed
 // order, so the codes are bit-exact.
 //
-// The exact sum of squares: a bf16 value is M 2^(e) with an 8-bit
-// significand M, so x^2 = M^2 2^te with M^2 < 2^16.  Squares with te in a
+// The mean square has to be the rounding of the exact one.  The register form
+// sums in fp64 and takes that where everything within its margin of error
+// rounds to the same fp32; the few rows where it does not, and the rows of the
+// other form, take the exact sum of squares: a bf16 value is M 2^(e) with an
+// 8-bit significand M, so x^2 = M^2 2^te with M^2 < 2^16.  Squares with te in a
 // window of 80 binary places go into a per-thread 128-bit fixed-point
 // accumulator (at most 2^15 terms below 2^96 each: no overflow); the rest
 // (tiny, huge, subnormal) go into per-exponent integer bins in shared memory.
