@@ -52,6 +52,7 @@ struct AttnParams {
     void *o;
     int64_t ldo;
     int o_bf16;
+    int o_vec;                        // four features of O at once: head_dim and ldo multiples of 4, O on their bytes
     float *lse;                       // or NULL
     float *part;                      // [grid, 2] partials
     uint32_t *status;
@@ -104,21 +105,25 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// a sequence's length, held to what its page list can hold
+// a sequence's length, held to what its page list can hold; EARLY: read before the launch's own wait, so from L2 (what
+// this SM's L1 holds may be older than the wait of the launch before)
+template <bool EARLY = false>
 __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
-    int64_t n = __ldg(p.lens + b);
+    int64_t n = EARLY ? __ldcg(p.lens + b) : __ldg(p.lens + b);
     const int64_t cap = p.max_pages << p.page_shift;
     return static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
 }
+template <bool EARLY>
 __device__ __forceinline__ int64_t units_of(const AttnParams &p, int b) {
-    return static_cast<int64_t>((length_of(p, b) + p.unit - 1) / p.unit) * p.vheads;
+    return static_cast<int64_t>((length_of<EARLY>(p, b) + p.unit - 1) / p.unit) * p.vheads;
 }
 
 // Totals over the sequences, by the whole CTA of 128 threads: the units of all, and of those before sequence `upto`.
+template <bool EARLY>
 __device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *before, int64_t *s_warp) {
     int64_t all = 0, pre = 0;
     for (int b = threadIdx.x; b < p.n_seqs; b += kWarps * 32) {
-        const int64_t n = units_of(p, b);
+        const int64_t n = units_of<EARLY>(p, b);
         all += n;
         if (b < upto) pre += n;
     }
@@ -144,12 +149,13 @@ __device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *before, int
 }
 
 // The sequence that holds unit u, and the units before it (*first): the CTA scans 128 sequences at a time.
+template <bool EARLY>
 __device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t *s_scan, int *s_at) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t before = 0;
     for (int b0 = 0; b0 < p.n_seqs; b0 += kWarps * 32) {
         const int b = b0 + threadIdx.x;
-        const int64_t mine = b < p.n_seqs ? units_of(p, b) : 0;
+        const int64_t mine = b < p.n_seqs ? units_of<EARLY>(p, b) : 0;
         int64_t s = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -196,18 +202,19 @@ struct Shares {
     int64_t units, start, first;   // units in all, first unit of the range, units before sequence b
     int ctas, b;
 };
+template <bool EARLY>
 __device__ Shares find_range(const AttnParams &p, int index, int64_t *s_scan, int *s_at) {
     Shares r;
     if (p.n_seqs > kWarps * 32) {
-        r.units = sum_units(p, 0, &r.first, s_scan);
+        r.units = sum_units<EARLY>(p, 0, &r.first, s_scan);
         r.ctas = static_cast<int>(r.units < p.grid ? r.units : p.grid);
         if (index >= r.ctas) return r;
         r.start = range_start(r.units, r.ctas, index);
-        r.b = find_seq(p, r.start, &r.first, s_scan, s_at);
+        r.b = find_seq<EARLY>(p, r.start, &r.first, s_scan, s_at);
         return r;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t mine = static_cast<int>(threadIdx.x) < p.n_seqs ? units_of(p, threadIdx.x) : 0;
+    const int64_t mine = static_cast<int>(threadIdx.x) < p.n_seqs ? units_of<EARLY>(p, threadIdx.x) : 0;
     int64_t s = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -233,6 +240,26 @@ __device__ Shares find_range(const AttnParams &p, int index, int64_t *s_scan, in
     r.first = s_scan[kWarps];
     r.b = *s_at;
     return r;
+}
+
+// four features of the output from element `at` on, the first `left` of them
+__device__ __forceinline__ void store4(const AttnParams &p, int64_t at, int left, const float (&x)[4]) {
+    if (p.o_vec) {   // rows and heads of whole fours on their alignment
+        if (p.o_bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (e >= left) break;
+        if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[at + e] = __float2bfloat16_rn(x[e]);
+        else static_cast<float *>(p.o)[at + e] = x[e];
+    }
 }
 
 // floats of one partial: per query head o in a row of head_dim rounded up to 4, then m and the sum of each
@@ -304,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 p.lse[static_cast<int64_t>(b) * p.n_heads + i] = -INFINITY;
     }
 
-    const Shares share = find_range(p, blockIdx.x, sh.scan, &sh.at);
+    const Shares share = find_range<false>(p, blockIdx.x, sh.scan, &sh.at);
     if (static_cast<int>(blockIdx.x) >= share.ctas) return;   // every CTA that works gets a unit
     const int todo = static_cast<int>(range_start(share.units, share.ctas, blockIdx.x + 1) - share.start);
     Walker at;   // the unit being worked on
@@ -697,37 +724,40 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                     }
                 }
                 __syncthreads();
-                for (int i = threadIdx.x; i < mine * kF; i += kWarps * 32) {
-                    const int h = i / kF, d = f0 + i % kF;
-                    float top = sh.m[0][h];
+                // four features of a head per thread and step
+                for (int i = threadIdx.x; i < mine * (kF / 4); i += kWarps * 32) {
+                    const int h = i / (kF / 4), at4 = 4 * (i % (kF / 4)), d = f0 + at4;
+                    if (d >= row) continue;
+                    float mw[kWarps];
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.m[w][h]);
+                    for (int w = 0; w < kWarps; ++w) mw[w] = sh.m[w][h];
+                    const float top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
                     const float z = top == -INFINITY ? 0.0f : top;
-                    float sum = 0.0f, x = 0.0f;
+                    float sum = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float f = exp2_fast(sh.m[w][h] - z);
-                        sum += f * sh.l[w][h];
-                        x += f * sh.o[w][h][i % kF];
+                        const float4 v = *reinterpret_cast<const float4 *>(&sh.o[w][h][at4]);
+                        const float f = exp2_fast(mw[w] - z);
+                        sum = fmaf(f, sh.l[w][h], sum);
+                        x[0] = fmaf(f, v.x, x[0]);
+                        x[1] = fmaf(f, v.y, x[1]);
+                        x[2] = fmaf(f, v.z, x[2]);
+                        x[3] = fmaf(f, v.w, x[3]);
                     }
                     const int64_t head = head0 + 8 * n + h;
-                    if (d < p.head_dim) {
-                        if (!whole) {
-                            part[(8 * n + h) * row + d] = x;
-                        } else {
-                            x *= sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-                            if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[b * p.ldo + head * p.head_dim + d] = __float2bfloat16_rn(x);
-                            else static_cast<float *>(p.o)[b * p.ldo + head * p.head_dim + d] = x;
-                        }
-                    }
-                    if (d == 0) {
-                        if (!whole) {
+                    if (!whole) {
+                        *reinterpret_cast<float4 *>(part + (8 * n + h) * row + d) = make_float4(x[0], x[1], x[2], x[3]);
+                        if (d == 0) {
                             part[p.per_vhead * row + 2 * (8 * n + h)] = top;
                             part[p.per_vhead * row + 2 * (8 * n + h) + 1] = sum;
-                        } else if (p.lse) {
-                            p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
                         }
+                        continue;
                     }
+                    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] *= inv;
+                    store4(p, b * p.ldo + head * p.head_dim + d, p.head_dim - d, x);
+                    if (d == 0 && p.lse) p.lse[static_cast<int64_t>(b) * p.n_heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
                 }
             }
         }
@@ -745,12 +775,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
     __shared__ float s_top[kWarps], s_sum[kWarps];
     __shared__ float4 s_o[kWarps][64];
     const int i0 = blockIdx.x, h = blockIdx.y;
-    const Shares next = find_range(p, i0 + 1, s_scan, &s_at);   // behind CTA i0's range
+    const Shares next = find_range<true>(p, i0 + 1, s_scan, &s_at);   // behind CTA i0's range
     bool mine = i0 + 1 < next.ctas, late = false;
     int b = 0, head = 0, i1 = 0;
     if (mine) {
         b = next.b;
-        const int64_t n_units = (length_of(p, b) + p.unit - 1) / p.unit;
+        const int64_t n_units = (length_of<true>(p, b) + p.unit - 1) / p.unit;
         const int vh = static_cast<int>(quotient(next.start - next.first, n_units)), sub = vh % p.vper;
         const int64_t first = next.first + vh * n_units, begin = range_start(next.units, next.ctas, i0);
         head = vh / p.vper * p.group + sub * p.per_vhead + h;
@@ -925,6 +955,7 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
     p.q_vec = c.head_dim % 8 == 0 && ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(Q) & 15) == 0   ? 16
               : c.head_dim % 4 == 0 && ldq % 4 == 0 && (reinterpret_cast<uintptr_t>(Q) & 7) == 0 ? 8
                                                                                                  : 2;
+    p.o_vec = c.head_dim % 4 == 0 && ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(O) & (o_bf16 ? 7 : 15)) == 0 ? 1 : 0;
     // 32 keys at once and two to four CTAs per SM; at 256 features 16 keys, so that two CTAs fit
     if (c.head_dim <= 64) return by_heads<1, 32, 4>(p, s);
     if (c.head_dim <= 128) return by_heads<2, 32, 3>(p, s);
