@@ -467,25 +467,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     };
 
     // Q fragments: column g of tile n is query head 8 n + g of the virtual head; piece i of lane (g, t) is
-    // features 32 i + 8 t .. + 7, the same that the lane holds of a key
+    // features 32 i + 8 t .. + 7, the same that the lane holds of a key.  With rows on 16 bytes the loads are
+    // unconditional, so that nothing waits for them before their use: a column behind the last head repeats it (what
+    // becomes of it is not written), and a piece behind head_dim repeats the last (it meets zeros of the keys).
     uint4 qf[NT][D / 32];
     auto load_q = [&](const Walker &w) {
         const int head0 = w.head0(p), heads = w.heads(p);
+        const uint16_t *row = reinterpret_cast<const uint16_t *>(p.q) + w.b * p.ldq + static_cast<int64_t>(head0) * p.head_dim;
+        if (p.q_vec == 16) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(row + min(8 * n + g, heads - 1) * p.head_dim);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) qf[n][i] = __ldg(src + (FULL ? 4 * i + t : min(4 * i + t, last_piece)));
+            }
+            return;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const int h = 8 * n + g, f = 32 * i + 8 * t;
                 uint32_t x[4] = {0u, 0u, 0u, 0u};
-                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + w.b * p.ldq +
-                                      static_cast<int64_t>(head0 + h) * p.head_dim + f;
+                const uint16_t *src = row + h * p.head_dim + f;
                 if (h < heads) {
-                    if (p.q_vec == 16) {
-                        if (FULL || f < p.head_dim) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
-                            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                        }
-                    } else if (p.q_vec == 8) {
+                    if (p.q_vec == 8) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             if (f + 4 * e < p.head_dim) {
