@@ -7,7 +7,8 @@
 // Bound: HBM.  Every key and value is read once and used for the few query
 // heads that share it, a handful of operations per byte.  So:
 //  * The work of a call, in units of 128 keys of one key-value head, is cut into
-//    one equal contiguous range per CTA (whatever the lengths are), and a CTA
+//    one equal contiguous range per CTA (whatever the lengths are; the end of a
+//    head counts as half a unit where there are many), and a CTA
 //    writes an unnormalised partial (m, sum, o) for a head whose keys it holds
 //    only a part of; a second small launch joins those.  The cut depends only
 //    on the lengths, so results repeat bit for bit.
@@ -56,7 +57,7 @@ struct AttnParams {
     float *lse;                       // or NULL
     float *part;                      // [grid, 2] partials
     uint32_t *status;
-    int unit;                         // keys per unit
+    int unit_shift;                   // log2 of the keys per unit
     int shift;                        // rows of the ring have a chunk to spare, and pages hold whole sectors (see the kernel)
     int q_vec;                        // bytes on which Q's rows and heads lie: 16, 8 or 2
     int grid;                         // CTAs of the first launch (those behind the number of units stay idle)
@@ -114,77 +115,8 @@ __device__ __forceinline__ int length_of(const AttnParams &p, int b) {
     return static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
 }
 template <bool EARLY>
-__device__ __forceinline__ int64_t units_of(const AttnParams &p, int b) {
-    return static_cast<int64_t>((length_of<EARLY>(p, b) + p.unit - 1) / p.unit) * p.vheads;
-}
-
-// Totals over the sequences, by the whole CTA of 128 threads: the units of all, and of those before sequence `upto`.
-template <bool EARLY>
-__device__ int64_t sum_units(const AttnParams &p, int upto, int64_t *before, int64_t *s_warp) {
-    int64_t all = 0, pre = 0;
-    for (int b = threadIdx.x; b < p.n_seqs; b += kWarps * 32) {
-        const int64_t n = units_of<EARLY>(p, b);
-        all += n;
-        if (b < upto) pre += n;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        pre += __shfl_xor_sync(0xffffffffu, pre, o);
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        s_warp[threadIdx.x >> 5] = all;
-        s_warp[kWarps + (threadIdx.x >> 5)] = pre;
-    }
-    __syncthreads();
-    all = pre = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        all += s_warp[i];
-        pre += s_warp[kWarps + i];
-    }
-    *before = pre;
-    return all;
-}
-
-// The sequence that holds unit u, and the units before it (*first): the CTA scans 128 sequences at a time.
-template <bool EARLY>
-__device__ int find_seq(const AttnParams &p, int64_t u, int64_t *first, int64_t *s_scan, int *s_at) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.n_seqs; b0 += kWarps * 32) {
-        const int b = b0 + threadIdx.x;
-        const int64_t mine = b < p.n_seqs ? units_of<EARLY>(p, b) : 0;
-        int64_t s = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += x;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) *s_at = -1;
-        if (lane == 31) s_scan[warp] = s;
-        __syncthreads();
-        int64_t all = 0, base = before;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) base += s_scan[i];
-            all += s_scan[i];
-        }
-        const int64_t end = base + s, start = end - mine;
-        if (start <= u && u < end) {
-            *s_at = b;
-            s_scan[kWarps] = start;
-        }
-        __syncthreads();
-        if (*s_at >= 0) {
-            *first = s_scan[kWarps];
-            return *s_at;
-        }
-        before += all;
-    }
-    return p.n_seqs;   // not reached for u below the total
+__device__ __forceinline__ int units_of(const AttnParams &p, int b) {
+    return (length_of<EARLY>(p, b) + (1 << p.unit_shift) - 1) >> p.unit_shift;
 }
 
 // a / b of non-negative values; 32-bit where they fit (a 64-bit division takes a few hundred cycles)
@@ -193,48 +125,109 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
-// first unit of CTA i's range
-__device__ __forceinline__ int64_t range_start(int64_t units, int ctas, int i) { return quotient(units * i, ctas); }
-
-// Where CTA range `index` begins: *units in all, *ctas that work, and for index < *ctas the sequence and the units
-// before it.  Up to 128 sequences take one look at the lengths, more of them two passes.
-struct Shares {
-    int64_t units, start, first;   // units in all, first unit of the range, units before sequence b
-    int ctas, b;
+// The cut: all units in a row, sequence by sequence and head by head, each at a place; CTA i works on the units whose
+// place lies in [i places / ctas, (i + 1) places / ctas).  Few units lie at consecutive places.  With four and more per
+// CTA a unit takes two places and the end of a head one more: that costs about half a unit (1.0 of 1.6 us), and ranges
+// of many short heads would take longer than the others.
+struct Cut {
+    int64_t places;   // in all
+    int ctas, many;   // CTAs that work; 1: two places per unit and one per head's end
+    __device__ __forceinline__ int64_t start(int i) const { return quotient(places * i, ctas); }   // of CTA i's range
+    __device__ __forceinline__ int64_t of(int64_t units, int64_t heads) const { return (units << many) + (many ? heads : 0); }
+    __device__ __forceinline__ int step() const { return 1 << many; }
 };
-template <bool EARLY>
-__device__ Shares find_range(const AttnParams &p, int index, int64_t *s_scan, int *s_at) {
-    Shares r;
-    if (p.n_seqs > kWarps * 32) {
-        r.units = sum_units<EARLY>(p, 0, &r.first, s_scan);
-        r.ctas = static_cast<int>(r.units < p.grid ? r.units : p.grid);
-        if (index >= r.ctas) return r;
-        r.start = range_start(r.units, r.ctas, index);
-        r.b = find_seq<EARLY>(p, r.start, &r.first, s_scan, s_at);
-        return r;
-    }
+// Where range `index` begins (for index < cut.ctas): its first place, the sequence there, and the places before that.
+struct Share {
+    Cut cut;
+    int64_t start, first;
+    int b;
+};
+
+// Sums over the CTA's 128 threads of n (at most 2^24), low word, and of n > 0, high word: in all, and up to this thread.
+__device__ __forceinline__ uint64_t scan_units(uint32_t n, uint64_t &upto, int64_t *s_scan) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t mine = static_cast<int>(threadIdx.x) < p.n_seqs ? units_of<EARLY>(p, threadIdx.x) : 0;
-    int64_t s = mine;
+    const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+    uint32_t s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += x;
     }
-    if (lane == 31) s_scan[warp] = s;
+    upto = static_cast<uint64_t>(__popc(some & (0xffffffffu >> (31 - lane)))) << 32 | s;
+    if (lane == 31) s_scan[warp] = static_cast<int64_t>(upto);
     __syncthreads();
-    r.units = 0;
+    uint64_t all = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) s += s_scan[i];
-        r.units += s_scan[i];
+        if (i < warp) upto += static_cast<uint64_t>(s_scan[i]);
+        all += static_cast<uint64_t>(s_scan[i]);
     }
-    r.ctas = static_cast<int>(r.units < p.grid ? r.units : p.grid);
-    if (index >= r.ctas) return r;   // the same for the whole CTA
-    r.start = range_start(r.units, r.ctas, index);
-    if (s - mine <= r.start && r.start < s) {
-        s_scan[kWarps] = s - mine;
+    return all;
+}
+
+__device__ __forceinline__ Cut make_cut(const AttnParams &p, int64_t units, int64_t heads) {
+    Cut c;
+    units *= p.vheads;
+    c.many = units >= 4ll * p.grid ? 1 : 0;
+    c.places = c.of(units, heads * p.vheads);
+    c.ctas = static_cast<int>(units < p.grid ? units : p.grid);
+    return c;
+}
+
+// more than 128 sequences: two passes over them
+template <bool EARLY>
+__device__ __forceinline__ Share find_range_of_many(const AttnParams &p, int index, int64_t *s_scan, int *s_at) {
+    Share r;
+    int64_t units = 0, heads = 0;
+    uint64_t upto;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += kWarps * 32) {
+        const int b = b0 + threadIdx.x;
+        const uint64_t all = scan_units(b < p.n_seqs ? units_of<EARLY>(p, b) : 0, upto, s_scan);
+        units += static_cast<uint32_t>(all);
+        heads += static_cast<int64_t>(all >> 32);
+        __syncthreads();
+    }
+    r.cut = make_cut(p, units, heads);
+    if (index >= r.cut.ctas) return r;   // the same for the whole CTA
+    r.start = r.cut.start(index);
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += kWarps * 32) {
+        const int b = b0 + threadIdx.x;
+        const int n = b < p.n_seqs ? units_of<EARLY>(p, b) : 0;
+        if (threadIdx.x == 0) *s_at = -1;
+        const uint64_t all = scan_units(n, upto, s_scan);
+        const int64_t end = before + r.cut.of(static_cast<uint32_t>(upto), upto >> 32) * p.vheads;
+        const int64_t first = end - (n > 0 ? r.cut.of(n, 1) * p.vheads : 0);
+        if (first <= r.start && r.start < end) {
+            *s_at = b;
+            s_scan[kWarps] = first;
+        }
+        __syncthreads();
+        if (*s_at >= 0) break;
+        before += r.cut.of(static_cast<uint32_t>(all), all >> 32) * p.vheads;
+        __syncthreads();
+    }
+    r.first = s_scan[kWarps];
+    r.b = *s_at;
+    return r;
+}
+
+// s_scan: kWarps + 1 values
+template <bool EARLY>
+__device__ __forceinline__ Share find_range(const AttnParams &p, int index, int64_t *s_scan, int *s_at) {
+    if (p.n_seqs > kWarps * 32) return find_range_of_many<EARLY>(p, index, s_scan, s_at);
+    Share r;
+    const int n = static_cast<int>(threadIdx.x) < p.n_seqs ? units_of<EARLY>(p, threadIdx.x) : 0;
+    uint64_t upto;
+    const uint64_t all = scan_units(n, upto, s_scan);
+    r.cut = make_cut(p, static_cast<uint32_t>(all), all >> 32);
+    if (index >= r.cut.ctas) return r;   // the same for the whole CTA
+    r.start = r.cut.start(index);
+    const int64_t end = r.cut.of(static_cast<uint32_t>(upto), upto >> 32) * p.vheads;
+    const int64_t first = end - (n > 0 ? r.cut.of(n, 1) * p.vheads : 0);
+    if (first <= r.start && r.start < end) {
         *s_at = threadIdx.x;
+        s_scan[kWarps] = first;
     }
     __syncthreads();
     r.first = s_scan[kWarps];
@@ -274,17 +267,19 @@ struct AttnShared {
     static constexpr int kFeatures = DB < 2 ? 64 : 128;
     float o[kWarps][8][kFeatures];
     float m[kWarps][8], l[kWarps][8];
-    int64_t scan[2 * kWarps];
+    int64_t scan[kWarps + 1];
     int at;
 };
 
-// A place in the list of units: sequence b (len keys, n units per head), part `sub` of the query heads of
-// key-value head kv, unit j of it.
+// A unit: sequence b (len keys, n units per head), part `sub` of the query heads of key-value head kv, unit j of it, and
+// its place counted from the first of this CTA's range.
 struct Walker {
-    int b, len, n, kv, sub, j;
-    __device__ __forceinline__ void next(const AttnParams &p) {
+    int b, len, n, kv, sub, j, place;
+    __device__ __forceinline__ void next(const AttnParams &p, const Cut &cut) {
+        place += cut.step();
         if (++j < n) return;
         j = 0;
+        place += cut.many;
         if (++sub < p.vper) return;
         sub = 0;
         if (++kv < p.n_kv) return;
@@ -292,7 +287,7 @@ struct Walker {
         do {   // sequences without keys have no units
             ++b;
             len = b < p.n_seqs ? length_of(p, b) : 0;
-            n = (len + p.unit - 1) / p.unit;
+            n = (len + (1 << p.unit_shift) - 1) >> p.unit_shift;
         } while (n == 0 && b < p.n_seqs);
     }
     __device__ __forceinline__ int head0(const AttnParams &p) const { return kv * p.group + sub * p.per_vhead; }
@@ -331,17 +326,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 p.lse[static_cast<int64_t>(b) * p.n_heads + i] = -INFINITY;
     }
 
-    const Shares share = find_range<false>(p, blockIdx.x, sh.scan, &sh.at);
-    if (static_cast<int>(blockIdx.x) >= share.ctas) return;   // every CTA that works gets a unit
-    const int todo = static_cast<int>(range_start(share.units, share.ctas, blockIdx.x + 1) - share.start);
+    const Share share = find_range<false>(p, blockIdx.x, sh.scan, &sh.at);
+    const Cut &cut = share.cut;
+    if (static_cast<int>(blockIdx.x) >= cut.ctas) return;   // every CTA that works gets a unit
+    const int todo = static_cast<int>(cut.start(blockIdx.x + 1) - share.start);   // places
     Walker at;   // the unit being worked on
     at.b = share.b;
     at.len = length_of(p, at.b);
     at.n = (at.len + kUnit - 1) / kUnit;
-    const int vhead = static_cast<int>(quotient(share.start - share.first, at.n));
+    const int vhead = static_cast<int>(quotient(share.start - share.first, cut.of(at.n, 1)));
     at.kv = vhead / p.vper;
     at.sub = vhead % p.vper;
-    at.j = static_cast<int>(share.start - share.first - static_cast<int64_t>(vhead) * at.n);
+    at.j = 0;
+    at.place = 0;
+    const int inside = static_cast<int>(share.start - share.first - vhead * cut.of(at.n, 1));   // places of the head before the range
+    if (inside > 0) {   // the first unit at or behind the range's start: in this head, or the next head's first
+        at.j = ((inside + cut.many) >> cut.many) - 1;
+        at.place = (at.j << cut.many) - inside;
+        at.next(p, cut);
+    }
 
     // A piece in the ring: rows of 128-byte segments (segment d of row r at (r DB + d) 128).  Copies: eight lanes take
     // a segment, 16 bytes each.  The 16-byte chunk k of a segment lies at k ^ 4 (r & 1) for K, k ^ (r & 6) for V, so
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         }
     };
     auto issue_k = [&]() {
-        if (copied < todo) {
+        if (ahead.place < todo) {
             const int key = ahead.j * kUnit + KT * warp;
             uint32_t ok = 0;
             if (one_page) {
@@ -453,12 +456,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         cp_commit();
     };
     auto issue_v = [&]() {
-        if (copied < todo) {
+        if (ahead.place < todo) {
             const int key = ahead.j * kUnit + KT * warp;
             if (key < ahead.len) copy(vh, true, key, bits >> (8 * (copied & 3)));
             slot = slot + 1 == ST ? 0 : slot + 1;
-            if (++copied < todo) {
-                ahead.next(p);
+            ++copied;
+            ahead.next(p, cut);
+            if (ahead.place < todo) {
                 if (ahead.j == 0) enter();
                 look_up();
             }
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
     float o[NT][DB][4][4];
     float m[NT][2], l[NT][2];
     int use = 0, seg_from = 0;   // ring slot of the next piece to be used; unit that began this head
-    for (int done = 0; done < todo; ++done) {
+    for (int done = 0;; ++done) {
         if (done == seg_from) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -686,8 +690,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         if (ST == 4) issue_k(); else issue_v();
 
         const bool ends = at.j + 1 == at.n;
-        if (!ends && done + 1 < todo) {
+        const bool more = at.place + cut.step() + (ends ? cut.many : 0) < todo;   // a unit is left in the range
+        if (!ends && more) {
             ++at.j;
+            at.place += cut.step();
             continue;
         }
         // The head ends here, or this CTA's range does: join the four warps through shared memory, while the copies
@@ -697,8 +703,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         const int b = at.b;
         float *part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg_from == 0 ? 0 : 1)) * part_floats(p.per_vhead, p.head_dim);
         const int row = part_row(p.head_dim);
-        if (done + 1 < todo) {
-            at.next(p);
+        if (more) {
+            at.next(p, cut);
             load_q(at);
         }
         seg_from = done + 1;
@@ -767,6 +773,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 }
             }
         }
+        if (!more) break;
     }
     cp_wait<0>();
 }
@@ -776,24 +783,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
 // the first launch: the lengths were complete before that one's CTAs let this launch begin.  A warp takes every fourth
 // partial, 32 of them at a time: lane j holds the j-th one's maximum and sum.
 __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParams p) {
-    __shared__ int64_t s_scan[2 * kWarps];
+    __shared__ int64_t s_scan[kWarps + 1];
     __shared__ int s_at;
     __shared__ float s_top[kWarps], s_sum[kWarps];
     __shared__ float4 s_o[kWarps][64];
     const int i0 = blockIdx.x, h = blockIdx.y;
-    const Shares next = find_range<true>(p, i0 + 1, s_scan, &s_at);   // behind CTA i0's range
-    bool mine = i0 + 1 < next.ctas, late = false;
+    const Share next = find_range<true>(p, i0 + 1, s_scan, &s_at);   // behind CTA i0's range
+    const Cut &cut = next.cut;
+    bool mine = i0 + 1 < cut.ctas, late = false;
     int b = 0, head = 0, i1 = 0;
     if (mine) {
         b = next.b;
-        const int64_t n_units = (length_of<true>(p, b) + p.unit - 1) / p.unit;
-        const int vh = static_cast<int>(quotient(next.start - next.first, n_units)), sub = vh % p.vper;
-        const int64_t first = next.first + vh * n_units, begin = range_start(next.units, next.ctas, i0);
+        const int n = units_of<true>(p, b);
+        const int vh = static_cast<int>(quotient(next.start - next.first, cut.of(n, 1))), sub = vh % p.vper;
+        const int64_t first = next.first + vh * cut.of(n, 1), begin = cut.start(i0);
+        const int64_t last = first + (static_cast<int64_t>(n - 1) << cut.many);   // places of the head's first and last unit
         head = vh / p.vper * p.group + sub * p.per_vhead + h;
-        mine = next.start > first && begin <= first && h < p.group - sub * p.per_vhead;
-        late = begin < first;   // the head is not the first of i0's range: its partial is in slot 1
-        // the CTA of the head's last unit: the largest i with range_start(i) below its end
-        i1 = static_cast<int>(quotient((first + n_units) * next.ctas - 1, next.units));
+        mine = next.start > first && begin <= first && next.start <= last && h < p.group - sub * p.per_vhead;
+        late = begin <= first - cut.many - cut.step();   // a unit of i0's range lies before the head: its partial is in slot 1
+        // the CTA of the head's last unit: the largest i whose range starts at its place or before
+        i1 = static_cast<int>(quotient((last + 1) * cut.ctas - 1, cut.places));
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -900,8 +909,10 @@ cudaError_t go(AttnParams p, cudaStream_t s) {
         if (occ > kAttnMaxCtas) occ = kAttnMaxCtas;
         occupancy.store(occ, std::memory_order_relaxed);
     }
-    p.unit = KT * kWarps;
-    const int64_t most = (((p.max_pages << p.page_shift) + p.unit - 1) / p.unit) * p.n_seqs * p.vheads;
+    constexpr int unit = KT * kWarps;
+    p.unit_shift = unit == 128 ? 7 : 6;
+    static_assert(unit == 128 || unit == 64, "the shift above");
+    const int64_t most = (((p.max_pages << p.page_shift) + unit - 1) / unit) * p.n_seqs * p.vheads;
     const int64_t room = static_cast<int64_t>(num_sms()) * occ;
     p.grid = static_cast<int>(most < room ? most : room);
     cudaLaunchAttribute attr[1];
@@ -916,7 +927,7 @@ cudaError_t go(AttnParams p, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, KT, ST, FULL>, p);
     if (e != cudaSuccess) return e;
-    if (p.grid < 2 || (p.max_pages << p.page_shift) <= p.unit) return cudaSuccess;   // one CTA, or one unit per head at most: nothing to join
+    if (p.grid < 2 || (p.max_pages << p.page_shift) <= unit) return cudaSuccess;   // one CTA, or one unit per head at most: nothing to join
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(p.per_vhead));
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_paged_attn_join, p);

@@ -158,6 +158,13 @@ def test_many_sequences(bn):
     check_case(bn, Case([int(x) for x in r.permutation(np.arange(300) % 90)], 4, 2, 64, 16, seed=3))
 
 
+@pytest.mark.parametrize("n,longest,heads,kv,d", [(60, 300, 32, 32, 64), (130, 400, 32, 32, 24), (128, 700, 48, 16, 40), (150, 260, 40, 1, 128)])
+def test_many_short_heads(bn, n, longest, heads, kv, d):
+    """More than four units per CTA: ranges that begin inside heads, at their ends and at their beginnings."""
+    r = np.random.default_rng(n)
+    check_case(bn, Case([int(x) for x in r.integers(0, longest + 1, n)], heads, kv, d, 16, seed=n))
+
+
 def test_peaked_scores(bn):
     """Scores of both signs up to hundreds: weights that underflow, a maximum that moves late."""
     c = Case([777, 64, 129], 8, 2, 128, 16, seed=4, spread=4.0)
