@@ -223,8 +223,9 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeParams p) {
 // A persistent CTA takes rows blockIdx.x, + gridDim.x, ...: one producer warp brings whole rows and their rows of the
 // table into a ring in shared memory (bulk copies counted on an mbarrier) and looks up their places in the cache,
 // eight warps turn them and write them out.  What a CTA per row waits for one after the other (its start, the
-// position, the page, the features) then lies behind the rows before it: with 4084 rows of 96 heads of 128 the direct
-// form above takes 48 us, whatever its share of registers and loads in flight.
+// position, the page, the features) then lies behind the rows before it: 4096 rows of 96 heads of 128 into the
+// cache take 39.7 us (5.1 TB/s) here and 50.6 in the direct form above, whatever its share of registers and loads in
+// flight; of 100, whose rows of 200 bytes leave a sector in seven partly written, 45.9 and 66.5.
 constexpr int kRowWarps = 8;
 constexpr int kRowSlots = 3;
 
@@ -453,16 +454,21 @@ cudaError_t go(RopeParams p, cudaStream_t s) {
     const int64_t row_bytes = static_cast<int64_t>(all) * p.head_dim * static_cast<int64_t>(sizeof(TI));
     const int64_t slot_bytes = (row_bytes + p.rot * 4 + 127) / 128 * 128;
     const int64_t smem = kRowSlots * slot_bytes + static_cast<int64_t>(sizeof(RowShared));
-    // Measured (direct / ring, us): 4084 cache rows of 96 heads of 128 48.4 / 42.5, of 100 63.8 / 41.5; 2048 rows of 64
-    // heads of 100 12.4 / 10.1; but 4095 fp32 rows of 64 x 128 41.3 / 46.6: rotation alone in 16-byte vectors stays direct.
-    if ((APPEND || VEC * sizeof(TI) < 16) && p.T >= 8 * num_sms() && smem <= 113 * 1024 && row_bytes % 16 == 0 && p.ldx * sizeof(TI) % 16 == 0 &&
-        (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.rot % 4 == 0 && (reinterpret_cast<uintptr_t>(p.table) & 15) == 0) {
+    // Measured (direct / ring, us).  Long rows: 4096 of 96 heads of 128 into the cache 50.6 / 39.7, 1200 of them 16.2 / 13.3,
+    // 4096 of 64 heads of 128 turned only 31.3 / 25.3; but 12 KB (4096 of 48 heads of 128) 26.0 / 26.1, 8 KB (30 heads)
+    // 17.4 / 24.2, 3 KB 7.2 / 18.6: a row's hand-over costs more than it hides.  Pieces narrower than 16 bytes, whatever the
+    // row: 4096 of 96 heads of 100 66.5 / 45.9, of 30 24.1 / 14.1, 600 of 64 5.0 / 4.9.  fp32 that stays fp32 has half the
+    // features per byte to turn and gains nothing: 4096 of 32 heads of 128 22.0 / 23.7, of 64 of 100 35.4 / 37.7.
+    const bool narrow = VEC * sizeof(TI) < 16;
+    if ((APPEND || sizeof(TI) == 2) && (narrow || row_bytes >= 16 * 1024) && p.T >= 8 * num_sms() && smem <= 113 * 1024 &&
+        row_bytes % 16 == 0 && p.ldx * sizeof(TI) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.rot % 4 == 0 &&
+        (reinterpret_cast<uintptr_t>(p.table) & 15) == 0) {
         p.row_bytes = static_cast<uint32_t>(row_bytes);
         p.slot_bytes = static_cast<uint32_t>(slot_bytes);
         p.slots = 32 * kRowWarps / p.places;
         // Two CTAs per SM with the registers for four heads in flight per thread, or three with fewer, so that the waits of
-        // short rows overlap.  Measured (two / three, us): 4084 rows of 96 heads of 96 (18 KB) 29.4 / 33.8, 16084 rows of 30
-        // heads of 128 (8 KB) 85.0 / 81.0, 8084 of 24 heads of 64 (3 KB) 37.9 / 33.7, 8192 of 64 heads of 100 (13 KB) 39.8 / 38.1.
+        // shorter rows overlap.  Measured (two / three, us): 4084 rows of 96 heads of 96 (18 KB) 29.4 / 33.8, 8192 of 64 heads
+        // of 100 (13 KB) 39.8 / 38.1.
         return row_bytes > 16 * 1024 || smem > 74 * 1024 ? go_rows<TI, TO, VEC, INTERLEAVED, APPEND, 2>(p, smem, s)
                                                          : go_rows<TI, TO, VEC, INTERLEAVED, APPEND, 3>(p, smem, s);
     }

@@ -268,7 +268,8 @@ def test_refusals(bn):
         bn.bitnet_rope_append(x[:2], pos[:2], tab, W[0], W[1], pages)
 
 
-@pytest.mark.parametrize("heads,kv,d,rot", [(32, 32, 100, 100), (20, 5, 128, 128), (6, 2, 40, 24), (2, 1, 72, 0), (4, 4, 36, 20)])
+@pytest.mark.parametrize("heads,kv,d,rot", [(32, 32, 100, 100), (20, 5, 128, 128), (6, 2, 40, 24), (2, 1, 72, 0), (4, 4, 36, 20),
+                                            (40, 12, 128, 128), (60, 20, 128, 64)])
 @pytest.mark.parametrize("dtype,interleaved,layout", [(BF16, False, "heads first"), (F32, True, "rows first"), (BF16, True, "rows first")])
 def test_append_of_many_rows(bn, heads, kv, d, rot, dtype, interleaved, layout):
     """Enough rows for several per persistent CTA, with padding rows and rows of bad indexes among them."""
@@ -292,10 +293,10 @@ def test_append_of_many_rows(bn, heads, kv, d, rot, dtype, interleaved, layout):
     assert np.array_equal(host(K), Kr) and np.array_equal(host(V), Vr)
 
 
-@pytest.mark.parametrize("d,rot", [(100, 100), (100, 36), (128, 128), (50, 20)])
+@pytest.mark.parametrize("d,rot,heads", [(100, 100, 8), (100, 36, 8), (128, 128, 8), (50, 20, 8), (128, 128, 64), (128, 64, 70)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_rope_of_many_rows_in_place(bn, d, rot, dtype):
-    T, heads = 1500, 8
+def test_rope_of_many_rows_in_place(bn, d, rot, heads, dtype):
+    T = 1500
     r = np.random.default_rng(d + rot)
     x = r.normal(size=(T, heads * d)).astype(np.float32)
     x = bf16(x) if dtype == BF16 else x
