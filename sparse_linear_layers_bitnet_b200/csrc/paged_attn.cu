@@ -26,6 +26,11 @@
 //    split into a bf16 high and low part (two MMAs), which keeps 16 bits of it:
 //    with a single bf16 p its rounding alone would be as large as that of the
 //    bf16 output.  The tensor pipe is far from being the bound.
+//
+// Measured: 8 contexts of 65536 to 131072 keys, 20 heads on 5 of 128 features,
+// 314 us (6.7 TB/s); 24 ragged sequences of up to 4096 keys x 32 heads of 100,
+// 101 us (5.5 TB/s); 128 sequences of up to 500 keys, 32 heads on 8, 31 us (4.2
+// TB/s: the ends of heads); one sequence of 4001 keys 8.6 us.
 #include "common.cuh"
 #include "kernels.h"
 
