@@ -495,8 +495,8 @@ bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld
  * A sequence without keys (an idle slot of the batch) gets zeros and minus
  * infinity.  Rows of the cache behind a sequence's length are not used,
  * whatever they hold.  Scores, their maxima and sums and the output are held in
- * fp32, a softmax weight in 16 bits of significand; the result repeats bit for
- * bit.
+ * fp32, a softmax weight in fp32 too where O is fp32 and within 2^-17 of itself
+ * where O is bf16; the result repeats bit for bit.
  *
  *   Q         [n_seqs, ldq] bf16, n_heads * head_dim elements of a row are used.
  *   cache     host struct, read during the call only; n_heads % n_kv_heads == 0.

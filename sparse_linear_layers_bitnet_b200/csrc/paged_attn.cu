@@ -23,9 +23,18 @@
 //    The contraction index may be permuted at will, so K's fragments are the 16
 //    bytes a lane loaded, and V^T's are byte permutes of two rows' words.  S^T
 //    becomes the P^T operand by an 8 x 8 transpose per warp (movmatrix).  p is
-//    split into a bf16 high and low part (two MMAs), which keeps 16 bits of it:
-//    with a single bf16 p its rounding alone would be as large as that of the
-//    bf16 output.  The tensor pipe is far from being the bound.
+//    split into bf16 parts, one MMA each: with a single one its rounding alone
+//    would be as large as that of a bf16 output.  For an fp32 output three parts
+//    hold all its 24 bits; for bf16 two parts keep it within 2^-17, 1/256 of the
+//    output's own rounding (the third costs 2 to 5% where heads are short, 300
+//    sequences of up to 40 keys 28.7 against 29.8 us, and 6% with 16 query heads
+//    per key-value head).
+//  * The tensor core cuts its sums off: over a long chain of products that
+//    loses up to 2^-23 of the sum each time, always towards zero (6.8e-6 of the
+//    output at 3300 keys per warp).  So its accumulators hold the keys of one
+//    step only, the smallest parts first, and the running sums are rounded fp32
+//    additions (7.6e-8 there; no cost but 3 to 4% with 16 query heads per
+//    key-value head).
 //
 // Measured: 8 contexts of 65536 to 131072 keys, 20 heads on 5 of 128 features,
 // 314 us (6.7 TB/s); 24 ragged sequences of up to 4096 keys x 32 heads of 100,
@@ -35,6 +44,7 @@
 #include "kernels.h"
 
 #include <atomic>
+#include <limits>
 
 namespace bitnet {
 
@@ -54,7 +64,8 @@ struct AttnParams {
     int n_seqs, n_heads, group;       // group: query heads per key-value head
     int n_kv, vheads, vper, per_vhead;   // virtual key-value heads: vheads = n_kv x vper, each with up to per_vhead query heads
     int head_dim;
-    float scale_log2;                 // scale log2 e
+    float scale_log2;                 // scale log2 e, not zero
+    float none;                       // the infinity that scale_log2 turns into minus infinity: a key that is left out
     void *o;
     int64_t ldo;
     int o_bf16;
@@ -91,6 +102,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same without an accumulator before it
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -103,12 +121,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// high and low bf16 parts of a pair, packed
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
+// A pair of weights as PARTS bf16 parts each, packed.  Cutting keeps the leading 8 bits and leaves an exact rest of 16, then
+// of 8: three parts add up to all 24 bits of the weight.  Two parts, the second rounded, keep it within 2^-17.
+template <int PARTS>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[PARTS]) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        if (PARTS == 2 && i == 1) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            part[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            part[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+        }
+        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+    }
 }
 
 // a sequence's length, held to what its page list can hold; EARLY: read before the launch's own wait, so from L2 (what
@@ -300,8 +327,8 @@ struct Walker {
 };
 
 // DB: 64-feature blocks (head_dim <= 64 DB), NT: tiles of 8 query heads, KT: keys a warp takes at once (16 or 32),
-// ST: pieces (K or V of KT keys) in a warp's ring, FULL: head_dim is 64 DB
-template <int DB, int NT, int KT, int ST, bool FULL>
+// ST: pieces (K or V of KT keys) in a warp's ring, FULL: head_dim is 64 DB, PARTS: bf16 parts of a softmax weight
+template <int DB, int NT, int KT, int ST, bool FULL, int PARTS>
 __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams p) {
     constexpr int D = 64 * DB;
     constexpr int R = KT / 8;                       // groups of 8 keys: a page holds whole groups
@@ -584,10 +611,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
         use = use + 1 == ST ? 0 : use + 1;
         if (ST == 4) issue_v(); else issue_k();
 
-        // mask, running maximum, p
-        uint32_t ph[NT][M][2], pl[NT][M][2];
+        // mask, running maximum, p = 2^(s scale - maximum) with the product not rounded on its own
+        uint32_t ps[PARTS][NT][M][2];
         if (live) {
-            if ((now & kAll) != kAll || key + KT > at.len) {
+            if ((now & kAll) != kAll || key + KT > at.len) {   // the same for the whole warp
 #pragma unroll
                 for (int k = 0; k < M; ++k) {
                     const bool in0 = (now >> (2 * k) & 1u) && key + 16 * k + g < at.len;
@@ -595,23 +622,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) s[n][k][c] = (c < 2 ? in0 : in1) ? s[n][k][c] * p.scale_log2 : -INFINITY;
+                        for (int c = 0; c < 4; ++c) s[n][k][c] = (c < 2 ? in0 : in1) ? s[n][k][c] : p.none;
                 }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < M; ++k)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[n][k][c] *= p.scale_log2;
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float x0 = fmaxf(s[n][0][0], s[n][0][2]), x1 = fmaxf(s[n][0][1], s[n][0][3]);
+                float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-                for (int k = 1; k < M; ++k) {
-                    x0 = fmaxf(x0, fmaxf(s[n][k][0], s[n][k][2]));
-                    x1 = fmaxf(x1, fmaxf(s[n][k][1], s[n][k][3]));
+                for (int k = 0; k < M; ++k) {
+                    x0 = fmaxf(x0, fmaxf(s[n][k][0] * p.scale_log2, s[n][k][2] * p.scale_log2));
+                    x1 = fmaxf(x1, fmaxf(s[n][k][1] * p.scale_log2, s[n][k][3] * p.scale_log2));
                 }
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) {
@@ -640,20 +660,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
                 const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
                 for (int k = 0; k < M; ++k) {
-                    const float p0 = exp2_fast(s[n][k][0] - z0), p1 = exp2_fast(s[n][k][1] - z1);
-                    const float p2 = exp2_fast(s[n][k][2] - z0), p3 = exp2_fast(s[n][k][3] - z1);
-                    l[n][0] += p0 + p2;
-                    l[n][1] += p1 + p3;
-                    split2(p0, p1, ph[n][k][0], pl[n][k][0]);
-                    split2(p2, p3, ph[n][k][1], pl[n][k][1]);
-                }
-#pragma unroll
-                for (int k = 0; k < M; ++k)
+                    float w[2][2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        ph[n][k][r] = transpose8x8(ph[n][k][r]);
-                        pl[n][k][r] = transpose8x8(pl[n][k][r]);
+                        w[r][0] = exp2_fast(fmaf(s[n][k][2 * r], p.scale_log2, -z0));
+                        w[r][1] = exp2_fast(fmaf(s[n][k][2 * r + 1], p.scale_log2, -z1));
                     }
+                    l[n][0] += w[0][0] + w[1][0];
+                    l[n][1] += w[0][1] + w[1][1];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t part[PARTS];
+                        split<PARTS>(w[r][0], w[r][1], part);
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) ps[i][n][k][r] = transpose8x8(part[i]);
+                    }
+                }
             }
         }
 
@@ -667,25 +689,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn(const AttnParams 
             const uint32_t src = ring + use * kPiece + 2 * t * DB * 128;
             const uint32_t row0 = src + (c0 >> 3) * 128 + (((c0 & 7) ^ (2 * t)) << 4);
             const uint32_t row1 = src + DB * 128 + (c1 >> 3) * 128 + (((c1 & 7) ^ (2 * t)) << 4);
+            // in accumulators of this step's own (of 16 keys where two tiles of heads and three parts fill the registers)
+            constexpr int KC = NT == 1 || PARTS == 2 ? M : 1;
 #pragma unroll
-            for (int k = 0; k < M; ++k) {
+            for (int k0 = 0; k0 < M; k0 += KC) {
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     if (!FULL && 8 * d > last_piece) break;
-                    const uint32_t step = (16 * k * DB + d) * 128;
-                    const uint4 v0 = lds16(row0 + step), v1 = lds16(row1 + step);
-                    const uint4 v2 = lds16(row0 + step + 8 * DB * 128), v3 = lds16(row1 + step + 8 * DB * 128);
-                    const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-                    const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+                    uint32_t v[KC][4][4];   // rows 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
+#pragma unroll
+                    for (int k = 0; k < KC; ++k)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint4 x = lds16((r & 1 ? row1 : row0) + (16 * (k0 + k) * DB + d) * 128 + (r >> 1) * (8 * DB * 128));
+                            v[k][r][0] = x.x;
+                            v[k][r][1] = x.y;
+                            v[k][r][2] = x.z;
+                            v[k][r][3] = x.w;
+                        }
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         // rows g and g + 8 of the MMA are features 64 d + 8 g + 2 w and + 1
-                        const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
-                        const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+                        uint32_t a[KC][4];
+#pragma unroll
+                        for (int k = 0; k < KC; ++k)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                a[k][c] = __byte_perm(v[k][c & 2][w], v[k][(c & 2) + 1][w], c & 1 ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma(o[n][d][w], a0, a1, a2, a3, ph[n][k][0], ph[n][k][1]);
-                            mma(o[n][d][w], a0, a1, a2, a3, pl[n][k][0], pl[n][k][1]);
+                            float x[4];
+#pragma unroll
+                            for (int i = PARTS - 1; i >= 0; --i)
+#pragma unroll
+                                for (int k = 0; k < KC; ++k) {
+                                    const uint32_t(&pk)[2] = ps[i][n][k0 + k];
+                                    if (i == PARTS - 1 && k == 0) mma_first(x, a[k][0], a[k][1], a[k][2], a[k][3], pk[0], pk[1]);
+                                    else mma(x, a[k][0], a[k][1], a[k][2], a[k][3], pk[0], pk[1]);
+                                }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[n][d][w][c] += x[c];
                         }
                     }
                 }
@@ -897,18 +940,18 @@ int per_vhead_of(int64_t group, int64_t head_dim) {
     return static_cast<int>(group < most ? group : most);
 }
 
-template <int DB, int NT, int KT, int ST, bool FULL>
-cudaError_t go(AttnParams p, cudaStream_t s) {
+template <int DB, int NT, int KT, int ST, bool FULL, int PARTS>
+cudaError_t go_parts(AttnParams p, cudaStream_t s) {
     constexpr int smem = kWarps * ST * KT * 64 * DB * 2 + static_cast<int>(sizeof(AttnShared<DB>));
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
     p.shift = !FULL && (p.head_dim + 7) / 8 < 8 * DB && p.page_stride % 16 == 0 ? 1 : 0;
-    const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, KT, ST, FULL>);
+    const void *f = reinterpret_cast<const void *>(k_paged_attn<DB, NT, KT, ST, FULL, PARTS>);
     cudaError_t e = smem_attr(f, smem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> occupancy{0};   // the same on every device of this architecture
     int occ = occupancy.load(std::memory_order_relaxed);
     if (occ == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_paged_attn<DB, NT, KT, ST, FULL>, kWarps * 32, smem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_paged_attn<DB, NT, KT, ST, FULL, PARTS>, kWarps * 32, smem);
         if (e != cudaSuccess) return e;
         if (occ < 1) occ = 1;
         if (occ > kAttnMaxCtas) occ = kAttnMaxCtas;
@@ -930,12 +973,17 @@ cudaError_t go(AttnParams p, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, KT, ST, FULL>, p);
+    e = cudaLaunchKernelEx(&cfg, k_paged_attn<DB, NT, KT, ST, FULL, PARTS>, p);
     if (e != cudaSuccess) return e;
     if (p.grid < 2 || (p.max_pages << p.page_shift) <= unit) return cudaSuccess;   // one CTA, or one unit per head at most: nothing to join
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(p.per_vhead));
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_paged_attn_join, p);
+}
+
+template <int DB, int NT, int KT, int ST, bool FULL>
+cudaError_t go(const AttnParams &p, cudaStream_t s) {
+    return p.o_bf16 ? go_parts<DB, NT, KT, ST, FULL, 2>(p, s) : go_parts<DB, NT, KT, ST, FULL, 3>(p, s);
 }
 
 template <int DB, int KT, int ST>
@@ -970,7 +1018,9 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
     p.n_kv = c.n_kv_heads;
     p.vheads = p.n_kv * p.vper;
     p.head_dim = c.head_dim;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    if (p.scale_log2 == 0.0f) p.scale_log2 = std::numeric_limits<float>::denorm_min();   // weights of 1 all the same
+    p.none = p.scale_log2 < 0.0f ? INFINITY : -INFINITY;
     p.o = O; p.o_bf16 = o_bf16 ? 1 : 0; p.ldo = ldo; p.lse = lse;
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
     p.status = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kStatusOffset);

@@ -296,3 +296,44 @@ def test_refusals(bn):
         bn.bitnet_paged_attn(q, K, V, pages, lens, ws=bn.Workspace(256))
     e = bn.bitnet_paged_attn(q[:0], K, V, pages[:0], lens[:0])
     assert e.shape == (0, 256)
+
+
+def test_long_sums_are_rounded_not_cut(bn):
+    """Equal weights, and in feature f one value of 1 at key 2048 f among values of 2^-28: 32 of those are one step of
+    fp32 at 1.  A chain of 16 key products that cuts off instead of rounding loses every 16 of them.
+
+    Bound of O n (n = 2^18 keys, so weights are 2^-18 and n O is 1 + 2^-10): the 32 keys around the 1 lose less than
+    2^-23, every other step of 32 keys adds a multiple of 2^-23 exactly; the joins of four warps and of at most 74
+    ranges per head (a quarter of them in one warp) are 4 + 19 + 4 rounded additions; a reciprocal, a product and a
+    rounding to fp32: 32 u in all, and 2^-10 of them."""
+    n, d, page, kv, B = 1 << 18, 128, 64, 2, 4
+    K = torch.zeros((n // page, kv, page, d), dtype=BF16, device="cuda")
+    V = torch.full((n // page, page, d), 2.0 ** -28, device="cuda")
+    V.view(n, d)[2048 * torch.arange(d, device="cuda"), torch.arange(d, device="cuda")] = 1.0
+    V = V.to(BF16)[:, None].expand(-1, kv, -1, -1).contiguous()
+    pages = torch.arange(n // page, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = torch.ones((B, 4 * kv * d), dtype=BF16, device="cuda")
+    O = bn.bitnet_paged_attn(q, K, V, pages, torch.full((B,), n, dtype=torch.int32, device="cuda"), o_dtype=F32)
+    err = np.abs(host(O) * n - (1 + (n - 1) * 2.0 ** -28))
+    assert err.max() <= 32 * U * (1 + 2.0 ** -9), err.max() / U
+
+
+def test_weights_keep_24_bits(bn):
+    """Two keys of one feature, q = 1 and scale 1: x = k, the first key's value 0 and its score the larger, the second's
+    value 1, so O = p / (1 + p) with p = 2^(x log2 e - m).  Roundings of p: log2 e (u |x|), the maximum (u, |m| <= 1.45,
+    which cancels in p only where it is the same for both keys: it is), the exponent (u |x - m| <= 2.9 u, times ln 2) and
+    2^-22 of the power: 2^-22 + 4.5 u; three parts of 8 bits hold p without a further one.  Then the sum, its reciprocal
+    and the product: 4 u."""
+    B, kv = 64, 32
+    r = np.random.default_rng(0)
+    x = np.stack([np.ones((B, kv)), r.uniform(-1, 1, (B, kv))], -1).astype(np.float32)
+    x = bf16(x)
+    K, V = (bn.kv_cache(B, kv, 8, 1) for _ in range(2))
+    K[:, :, :2, 0] = up(x, BF16)
+    V[:, :, 1] = 1.0
+    pages = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    O = bn.bitnet_paged_attn(torch.ones((B, kv), dtype=BF16, device="cuda"), K, V, pages.contiguous(),
+                             torch.full((B,), 2, dtype=torch.int32, device="cuda"), scale=1.0, o_dtype=F32)
+    p = np.exp(x[..., 1].astype(np.float64) - 1.0)
+    ref = p / (1 + p)
+    assert np.all(np.abs(host(O) - ref) <= ref * (2.0 ** -22 + 8.5 * U))
