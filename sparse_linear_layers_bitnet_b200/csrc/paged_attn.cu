@@ -122,9 +122,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // A pair of weights as PARTS bf16 parts each, packed.  Cutting keeps the leading 8 bits and leaves an exact rest of 16, then
-// of 8: three parts add up to all 24 bits of the weight.  Two parts, the second rounded, keep it within 2^-17.
+// of 8: three parts add up to all 24 bits of the weight.  Two parts, the second rounded, keep it within 2^-17.  A rest of
+// zero becomes 2^-126, which no sum here feels: zero times a value of Inf would be NaN, where the weight itself gives Inf.
 template <int PARTS>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[PARTS]) {
+    constexpr float kLeast = 1.17549435e-38f;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
         if (PARTS == 2 && i == 1) {
@@ -133,8 +135,8 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[PARTS])
         } else {
             part[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
         }
-        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+        a = fmaxf(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u), kLeast);
+        b = fmaxf(b - __uint_as_float(__float_as_uint(b) & 0xffff0000u), kLeast);
     }
 }
 
@@ -889,18 +891,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_join(const AttnParam
             if (c == 1 && row <= 128) break;
             const int at = 4 * (lane + 32 * c) < row ? 4 * (lane + 32 * c) : 0;   // lanes without features repeat the first
             for (int j = 0; j < n; j += 8) {
-                // eight loads with no condition, so that they are in flight together; those behind the last one count 0
+                // eight loads with no condition, so that they are in flight together; those behind the last one are not used
                 float4 v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     v[k] = *reinterpret_cast<const float4 *>(partial(j0 + kWarps * min(j + k, n - 1)) + h * row + at);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float fj = j + k < n ? __shfl_sync(0xffffffffu, fi, j + k) : 0.0f;
-                    o[c].x = fmaf(v[k].x, fj, o[c].x);
-                    o[c].y = fmaf(v[k].y, fj, o[c].y);
-                    o[c].z = fmaf(v[k].z, fj, o[c].z);
-                    o[c].w = fmaf(v[k].w, fj, o[c].w);
+                    const bool used = j + k < n;   // (0 times an Inf behind the last one would be NaN)
+                    const float fj = __shfl_sync(0xffffffffu, fi, j + k);
+                    o[c].x = used ? fmaf(v[k].x, fj, o[c].x) : o[c].x;
+                    o[c].y = used ? fmaf(v[k].y, fj, o[c].y) : o[c].y;
+                    o[c].z = used ? fmaf(v[k].z, fj, o[c].z) : o[c].z;
+                    o[c].w = used ? fmaf(v[k].w, fj, o[c].w) : o[c].w;
                 }
             }
         }

@@ -337,3 +337,44 @@ def test_weights_keep_24_bits(bn):
     p = np.exp(x[..., 1].astype(np.float64) - 1.0)
     ref = p / (1 + p)
     assert np.all(np.abs(host(O) - ref) <= ref * (2.0 ** -22 + 8.5 * U))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("heads,kv,d", [(4, 2, 128), (32, 2, 64), (3, 3, 100), (8, 1, 256)])
+def test_infinities_and_nan_in_keys_and_values(bn, heads, kv, d, dtype):
+    """A value of Inf gives Inf whatever its weight's bits are (1 and 1/2 among them), both signs or NaN give NaN, in that
+    feature only; a key whose score is minus infinity counts nothing, one of plus infinity or NaN makes its head NaN."""
+    lens = [40, 300, 5, 7, 64, 200]
+    c = Case(lens, heads, kv, d, 16, seed=11)
+    c.q[:] = np.where(np.arange(heads * d) % d == 0, 1.0, 0.0)     # scores come from feature 0
+    for b in range(len(lens)):
+        c.k[b][:, :, 0] = -np.arange(lens[b])[None] % 4              # weights 1, e^(-scale), ... : some of them bare powers
+    c.k[4][:, 3, 0] = -np.inf                                        # left out
+    c.k[5][:, 9, 0] = np.inf
+    c.v[0][:, 4, 1], c.v[0][:, 8, 2], c.v[0][:, 1, 3] = np.inf, -np.inf, np.inf
+    c.v[0][:, 2, 4], c.v[0][:, 6, 4] = np.inf, -np.inf
+    c.v[1][:, 299, d - 1], c.v[1][:, 0, 5], c.v[1][:, 150, 6] = np.inf, np.nan, -np.inf
+    for b, n in enumerate(lens):                                     # into the pages
+        for j in range(-(-n // 16)):
+            rows = slice(16 * j, min(n, 16 * j + 16))
+            c.K[c.pages[b, j], :, :rows.stop - rows.start].copy_(up(c.k[b][:, rows], BF16))
+            c.V[c.pages[b, j], :, :rows.stop - rows.start].copy_(up(c.v[b][:, rows], BF16))
+    O, lse = run(bn, c, dtype)
+    got, got_l = host(O).reshape(len(lens), heads, d), host(lse)
+    assert np.isnan(got[5]).all() and np.isnan(got_l[5]).all()
+    x = [np.einsum("hgd,hnd->hgn", np.ones((kv, heads // kv, 1)), c.k[b][:, :, :1].astype(np.float64)) * c.scale for b in range(5)]
+    p = [np.exp(s - s.max(-1, keepdims=True)) for s in x]
+    with np.errstate(invalid="ignore"):
+        ref = np.stack([np.einsum("hgn,hnd->hgd", w / w.sum(-1, keepdims=True), c.v[b].astype(np.float64)).reshape(heads, d)
+                        for b, w in enumerate(p)])
+    got = got[:5]
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(np.isposinf(got), np.isposinf(ref)) and np.array_equal(np.isneginf(got), np.isneginf(ref))
+    assert np.isposinf(ref[0, :, 1]).all() and np.isnan(ref[0, :, 4]).all() and np.isfinite(ref[4]).all()
+    size = np.stack([np.einsum("hgn,hnd->hgd", w / w.sum(-1, keepdims=True), np.abs(np.nan_to_num(c.v[b].astype(np.float64), posinf=0, neginf=0)))
+                     .reshape(heads, d) for b, w in enumerate(p)])
+    # scores are exact up to u |x|, |x| < 4: the weights within 2^-17 + 2^-21, twice that with their sum, then the rounding of O
+    ok = np.isfinite(ref)
+    bound = 2 * (2.0 ** -17 + 2.0 ** -20) * size
+    bound += (2.0 ** -8 if dtype == BF16 else U) * (np.abs(np.where(ok, ref, 0)) + bound)
+    assert np.all(np.abs(got[ok] - ref[ok]) <= bound[ok])
