@@ -48,11 +48,18 @@ __device__ __forceinline__ void add128_sq(uint64_t &lo, uint64_t &hi, uint64_t v
     lo = s;
 }
 
+// what a row holds besides squares in the window: squares in the bins, Inf, NaN
+constexpr int kRowBins = 1, kRowInf = 2, kRowNan = 4;
+
 // x^2 of one bf16 value (16 bits) into the window accumulator or the bins
 __device__ __forceinline__ void sq_accumulate(uint32_t b16, uint64_t &lo, uint64_t &hi,
                                               unsigned long long *s_bins, int *s_rare) {
     const uint32_t E = (b16 >> 7) & 0xffu, m7 = b16 & 0x7fu;
     if (E == 0u && m7 == 0u) return;                       // +-0
+    if (E == 255u) {                                       // no square, and no bin
+        atomicOr(s_rare, m7 ? kRowNan : kRowInf);
+        return;
+    }
     const uint32_t M = E ? (m7 | 0x80u) : m7;
     const int te = E ? 2 * static_cast<int>(E) - 268 : -266;
     const uint64_t M2 = static_cast<uint64_t>(M * M);
@@ -62,7 +69,7 @@ __device__ __forceinline__ void sq_accumulate(uint32_t b16, uint64_t &lo, uint64
         else add128_sq(lo, hi, 0ull, M2 << (sh - 64));
     } else {
         atomicAdd(&s_bins[te - kSqTeMin], static_cast<unsigned long long>(M2));
-        *s_rare = 1;
+        atomicOr(s_rare, kRowBins);
     }
 }
 
@@ -139,16 +146,28 @@ __device__ __forceinline__ float bf16_of(uint16_t b) { return __uint_as_float(st
 
 __device__ __forceinline__ float bf16_at(const uint16_t *p, int64_t i) { return bf16_of(__ldg(p + i)); }
 
+// the larger one; NaN where either is (fmaxf takes the other one)
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+template <bool OR_NAN>
+__device__ __forceinline__ float larger(float a, float b) {
+    return OR_NAN ? max_or_nan(a, b) : fmaxf(a, b);
+}
+
+template <bool OR_NAN = false>
 __device__ __forceinline__ float bq_block_max(float v, float *s_red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = larger<OR_NAN>(v, __shfl_xor_sync(0xffffffffu, v, o));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) s_red[warp] = v;
     __syncthreads();
     if (warp == 0) {
         v = lane < static_cast<int>(blockDim.x >> 5) ? s_red[lane] : 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = 16; o > 0; o >>= 1) v = larger<OR_NAN>(v, __shfl_xor_sync(0xffffffffu, v, o));
         if (lane == 0) s_red[0] = v;
     }
     __syncthreads();
@@ -233,7 +252,8 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *X,
     if (threadIdx.x == 0) {
         uint64_t L = 0, H = 0;
         for (int i = 0; i < kBqThreads / 32; ++i) add128_sq(L, H, s_lo[i], s_hi[i]);
-        const double S = sq_finalize(L, H, s_bins, s_rare != 0, s_limb);
+        double S = sq_finalize(L, H, s_bins, (s_rare & kRowBins) != 0, s_limb);
+        if (s_rare & (kRowInf | kRowNan)) S = s_rare & kRowNan ? NAN : INFINITY;
         const float ms = __double2float_rn(__ddiv_rn(S, static_cast<double>(K)));
         s_r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
         if (rinv) rinv[t] = s_r;
@@ -245,11 +265,12 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *X,
     for (int64_t i = threadIdx.x; i < K; i += kBqThreads) {
         float v = __fmul_rn((ADD ? bf16_of(row[i]) : bf16_at(row, i)), r);
         if (w) v = __fmul_rn(v, __ldg(w + i));
-        m = fmaxf(m, fabsf(v));
+        m = max_or_nan(m, fabsf(v));
     }
-    m = bq_block_max(m, s_red);
-    const float a = m > eps_a ? m : eps_a;
+    m = bq_block_max<true>(m, s_red);
+    const float a = m <= eps_a ? eps_a : m;   // NaN stays NaN
     const float s = __fdiv_rn(127.0f, a);
+    const bool codes = a < INFINITY;          // else there is no scale, and the codes are 0
     if (threadIdx.x == 0) amax[t] = a;
     int8_t *out = Xq + t * K;
     for (int64_t i0 = 4 * threadIdx.x; i0 < K; i0 += 4 * kBqThreads) {
@@ -258,7 +279,7 @@ __global__ void __launch_bounds__(kBqThreads) k_rmsnorm_quant(const uint16_t *X,
         for (int j = 0; j < 4; ++j) {
             float v = __fmul_rn((ADD ? bf16_of(row[i0 + j]) : bf16_at(row, i0 + j)), r);
             if (w) v = __fmul_rn(v, __ldg(w + i0 + j));
-            q |= bq_code(v, s) << (8 * j);
+            q |= (codes ? bq_code(v, s) : 0u) << (8 * j);
         }
         *reinterpret_cast<uint32_t *>(out + i0) = q;
     }
@@ -381,7 +402,7 @@ __device__ __forceinline__ void sq_rare_add(uint32_t b16, unsigned long long *s_
     const uint32_t M = E ? (m7 | 0x80u) : m7;
     const int te = E ? 2 * static_cast<int>(E) - 268 : -266;
     const int sh = te - kSqTe0;
-    if (M != 0u && !(E != 0u && sh >= 0 && sh < 80))
+    if (M != 0u && E != 255u && !(E != 0u && sh >= 0 && sh < 80))   // Inf and NaN have no bin
         atomicAdd(&s_bins[te - kSqTeMin], static_cast<unsigned long long>(M * M));
 }
 

@@ -140,3 +140,57 @@ def test_refusals(bn):
     buf = torch.zeros((6, 512), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(bn.BitnetError):   # overlaps X by two rows
         bn.bitnet_add_rmsnorm_quant(buf[:4], X, H=buf[2:])
+
+
+def _not_finite(bn, T, K, weighted, off, fused):
+    """Rows with Inf, -Inf, NaN, both infinities, squares that overflow fp32, a weight of NaN; against the definition:
+    ms is Inf or NaN, r = 1 / sqrt(ms) 0 or NaN, absmax the largest |x r w| with NaN where one is, and no codes then."""
+    r = np.random.default_rng(K)
+    X, R = (r.normal(size=(T, K)).astype(np.float32) for _ in range(2))
+    X[1, K // 2], X[2, K - 1], X[3, 0] = np.inf, -np.inf, np.nan
+    X[4, 5], X[4, K - 8] = np.inf, -np.inf
+    X[5, 1], X[5, 2] = np.nan, np.inf
+    X[6] *= np.float32(2.0 ** 66)                           # finite, mean square above the fp32 range
+    X[7, 3], R[7, 3] = 3e38, 3e38                           # the sum overflows
+    if not fused:
+        R[:] = 0.0
+        X[7, 3] = np.inf
+    Xd, Xh = bf16_dev(X)
+    Rd, Rh = bf16_dev(R)
+    wd = (torch.rand(K + 1, device="cuda") + 0.5)[1 if off else 0:][:K] if weighted else None
+    with np.errstate(all="ignore"):
+        if fused:
+            H, Xq, am, rinv = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=wd)
+        else:
+            rinv = torch.empty(T, device="cuda")
+            Xq, am = bn.bitnet_rmsnorm_quant(Xd, wd, rinv=rinv)
+            H = Xd
+        h = (Xh + Rh).astype(np.float32) if fused else Xh
+        hb = synth.bf16_bits_to_f32(synth.to_bf16_bits(np.where(np.isnan(h), np.float32(0), h)))
+        hb[np.isnan(h)] = np.nan
+        got = H.float().cpu().numpy()
+        assert np.array_equal(np.isnan(got), np.isnan(hb)) and np.array_equal(got[~np.isnan(hb)], hb[~np.isnan(hb)])
+        ms = (hb.astype(np.float64) ** 2).mean(1).astype(np.float32)
+        rr = (1 / np.sqrt(ms + np.float32(1e-6))).astype(np.float32)
+        a = np.abs(hb * rr[:, None] * (1 if wd is None else wd.cpu().numpy())).max(1)
+    bad = [1, 2, 3, 4, 5, 7]
+    am, rinv, Xq = am.cpu().numpy(), rinv.cpu().numpy(), Xq.cpu().numpy()
+    assert np.isnan(a[bad]).all() and np.isnan(am[bad]).all()
+    assert np.array_equal(np.isnan(rinv), np.isnan(rr)) and np.isnan(rr[[3, 5]]).all()
+    assert not rinv[[1, 2, 4, 6, 7]].any() and not rr[[1, 2, 4, 6, 7]].any()
+    assert not Xq[bad + [6]].any() and am[6] == np.float32(1e-5)
+    fine = np.setdiff1d(np.arange(T), bad + [6])            # the other rows are the oracle's, bit for bit
+    xn, ro = oracle.rmsnorm(hb[fine], 1e-6, None if wd is None else wd.cpu().numpy(), return_r=True)
+    q, ao = oracle.quant_act(xn, 1e-5)
+    assert np.array_equal(rinv[fine], ro) and np.array_equal(am[fine], ao) and np.array_equal(Xq[fine], q)
+    if wd is not None:                                      # a weight of NaN, or of Inf, is seen as well
+        for v in (float("nan"), float("inf")):
+            wd[K - 3] = v
+            _, Xq, am, rinv = bn.bitnet_add_rmsnorm_quant(Xd, Rd, w=wd)
+            assert not bool(torch.isfinite(am).any()) and not Xq.any() and np.array_equal(rinv.cpu().numpy()[fine], ro)
+
+
+@pytest.mark.parametrize("K,weighted,off", [(40000, True, False), (40000, False, False), (2560, True, True), (33000, True, True)])
+@pytest.mark.parametrize("fused", [True, False])
+def test_rows_that_are_not_finite_in_the_general_form(bn, K, weighted, off, fused):
+    _not_finite(bn, 9, K, weighted, off, fused)
