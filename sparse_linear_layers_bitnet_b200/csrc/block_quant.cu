@@ -338,6 +338,14 @@ __device__ __forceinline__ bool sq_window(uint32_t b16, uint64_t &lo, uint64_t &
     return M2 != 0ull;   // +-0 contributes nothing; subnormals and out-of-window squares are rare
 }
 
+// x^2 of a value that sq_window left out into its bin
+__device__ __forceinline__ void sq_rare_add(uint32_t b16, unsigned long long *s_bins, int *s_rare) {
+    uint64_t lo, hi;
+    const uint32_t E = (b16 >> 7) & 0xffu;
+    const int sh = 2 * static_cast<int>(E) - 268 - kSqTe0;
+    if (E == 0u || sh < 0 || sh >= 80) sq_accumulate(b16, lo, hi, s_bins, s_rare);
+}
+
 // window (units 2^kSqTe0) += s for s > 0 an fp64 multiple of 2^kSqTe0 below 2^(kSqTe0 + 116)
 __device__ __forceinline__ void window_add_f64(double s, uint64_t &lo, uint64_t &hi) {
     const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s));
@@ -397,15 +405,6 @@ __device__ __forceinline__ double window_to_f64(uint64_t L, uint64_t H) {
     return __ull2double_rn(top) * __longlong_as_double(static_cast<long long>(1023 - 10 - lz) << 52);
 }
 
-__device__ __forceinline__ void sq_rare_add(uint32_t b16, unsigned long long *s_bins) {
-    const uint32_t E = (b16 >> 7) & 0xffu, m7 = b16 & 0x7fu;
-    const uint32_t M = E ? (m7 | 0x80u) : m7;
-    const int te = E ? 2 * static_cast<int>(E) - 268 : -266;
-    const int sh = te - kSqTe0;
-    if (M != 0u && E != 255u && !(E != 0u && sh >= 0 && sh < 80))   // Inf and NaN have no bin
-        atomicAdd(&s_bins[te - kSqTeMin], static_cast<unsigned long long>(M * M));
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -423,7 +422,7 @@ __device__ __forceinline__ uint2 codes8(const float *v, float s) {
     return q;
 }
 
-// block max for CTAs of up to 8 warps (s_red: 8 floats); one call per kernel
+// block max (s_red: one float per warp); one call per kernel
 __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -436,6 +435,70 @@ __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
     return r;   // every warp reduces the same values: no second barrier needed
 }
 
+// what the exact sum of a row needs
+struct SqShared {
+    unsigned long long bins[kSqBins];
+    unsigned long long lo[16], hi[16];
+    uint32_t limb[kSqLimbs];
+    float r;
+    int rare;
+};
+
+// The factor r of a row of K values by the exact sum of its squares; mine: this thread's n chunks of it (zeros behind the
+// row's end).  Called by the whole CTA for the few rows that need it, and kept out of line: inlined, its registers would be
+// every row's (40 -> 54 with two chunks per thread, 56 -> 96 with four: 12.9 -> 15.0 us at 2048 x 4096 with a residual).
+__device__ __noinline__ float exact_factor(const uint4 *mine, int n, int K, float eps_n, SqShared &sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    uint64_t lo = 0, hi = 0;
+    bool rare = false;
+    for (int j = 0; j < n; ++j) {
+        const uint4 v = mine[j];
+        if (sq_chunk_f64(v, lo, hi)) continue;
+        const uint32_t wv[4] = {v.x, v.y, v.z, v.w};   // a wide or out-of-window chunk: value by value
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            rare |= sq_window(wv[e] & 0xffffu, lo, hi);
+            rare |= sq_window(wv[e] >> 16, lo, hi);
+        }
+    }
+    if (threadIdx.x == 0) sh.rare = 0;
+    if (__syncthreads_or(rare)) {   // squares outside the window go to per-exponent bins (a second scan)
+        for (int i = threadIdx.x; i < kSqBins; i += blockDim.x) sh.bins[i] = 0ull;
+        __syncthreads();
+        if (rare) {
+            for (int j = 0; j < n; ++j) {
+                const uint4 v = mine[j];
+                const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sq_rare_add(wv[e] & 0xffffu, sh.bins, &sh.rare);
+                    sq_rare_add(wv[e] >> 16, sh.bins, &sh.rare);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+        add128_sq(lo, hi, l2, h2);
+    }
+    if (lane == 0) {
+        sh.lo[warp] = lo;
+        sh.hi[warp] = hi;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint64_t L = 0, H = 0;
+        for (int i = 0; i < nw; ++i) add128_sq(L, H, sh.lo[i], sh.hi[i]);
+        double S = sh.rare & kRowBins ? sq_finalize(L, H, sh.bins, true, sh.limb) : window_to_f64(L, H);
+        if (sh.rare & (kRowInf | kRowNan)) S = sh.rare & kRowNan ? NAN : INFINITY;
+        const float ms = __double2float_rn(__ddiv_rn(S, static_cast<double>(K)));
+        sh.r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
+    }
+    __syncthreads();
+    return sh.r;
+}
+
 // ADD: the row is bf16(X + R), formed in registers from both rows' loads and
 // written to H once (H may be X or R: a thread writes only what it alone has
 // read).  Per element 2 + 2 bytes in and 2 + 1 out.
@@ -445,12 +508,9 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
                                                          int K, double inv_k, float eps_n, float eps_a,
                                                          int8_t *__restrict__ Xq, float *__restrict__ amax,
                                                          float *__restrict__ rinv) {
-    __shared__ unsigned long long s_bins[kSqBins];
-    __shared__ unsigned long long s_lo[16], s_hi[16];
-    __shared__ uint32_t s_limb[kSqLimbs];
+    __shared__ SqShared s_exact;
     __shared__ float s_red[16];
     __shared__ double s_sq[16];
-    __shared__ float s_r;
     const int64_t t = blockIdx.x;
     const int nchunk = K >> 3;
     const uint4 *row = X + t * nchunk;
@@ -481,7 +541,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
     // S by fp64 fused multiply-adds.  At most 64 of them per thread, 5 steps in a warp and 16 over the warps: the sum is
     // within 2^-46 of the exact one, and so are 1/K and the product.  Where everything within 2^-44 of the quotient
     // rounds to the same fp32 (all but one row in 2^19), that is ms; else, and for tiny rows (zeros and subnormals are
-    // taken as about 2^-127 here), the exact sum below decides.
+    // taken as about 2^-127 here), the exact sum decides.
     double sq = 0.0;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
@@ -502,68 +562,18 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
     sq = s_sq[0];
     for (int i = 1; i < nw; ++i) sq += s_sq[i];
     const double q = sq * inv_k;
-    float ms = __double2float_rn(q * (1.0 - 0x1p-44));
-    const bool sure = q > 0x1p-120 && ms == __double2float_rn(q * (1.0 + 0x1p-44));
+    const float ms = __double2float_rn(q * (1.0 - 0x1p-44));
+    const bool sure = q > 0x1p-120 && ms == __double2float_rn(q * (1.0 + 0x1p-44));   // the same for every thread
     float r;
-    if (sure) {   // the same for every thread
+    if (sure) {
         r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
-        if (rinv && threadIdx.x == 0) rinv[t] = r;
     } else {
-        uint64_t lo = 0, hi = 0;
-        bool rare = false;
+        uint4 mine[CPT];
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-            if (!sq_chunk_f64(v[j], lo, hi)) {   // a wide or out-of-window chunk: value by value
-                const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    rare |= sq_window(wv[e] & 0xffffu, lo, hi);
-                    rare |= sq_window(wv[e] >> 16, lo, hi);
-                }
-            }
-        }
-        const bool any_rare = __syncthreads_or(rare) != 0;
-        if (any_rare) {   // squares outside the window go to per-exponent bins (a second scan of the registers)
-            for (int i = threadIdx.x; i < kSqBins; i += blockDim.x) s_bins[i] = 0ull;
-            __syncthreads();
-            if (rare) {
-#pragma unroll
-                for (int j = 0; j < CPT; ++j) {
-                    const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sq_rare_add(wv[e] & 0xffffu, s_bins);
-                        sq_rare_add(wv[e] >> 16, s_bins);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
-            add128_sq(lo, hi, l2, h2);
-        }
-        if (lane == 0) {
-            s_lo[warp] = lo;
-            s_hi[warp] = hi;
-        }
-        __syncthreads();
-        if (warp == 0) {   // one warp forms the total and r (its lanes in step), the others wait at the barrier
-            uint64_t L = 0, H = 0;
-            for (int i = 0; i < nw; ++i) add128_sq(L, H, s_lo[i], s_hi[i]);
-            double S;
-            if (!any_rare) S = window_to_f64(L, H);
-            else S = lane == 0 ? sq_finalize(L, H, s_bins, true, s_limb) : 0.0;
-            if (lane == 0) {
-                const float ms = __double2float_rn(__ddiv_rn(S, static_cast<double>(K)));
-                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
-                s_r = r;
-                if (rinv) rinv[t] = r;
-            }
-        }
-        __syncthreads();
-        r = s_r;
+        for (int j = 0; j < CPT; ++j) mine[j] = v[j];
+        r = exact_factor(mine, CPT, K, eps_n, s_exact);
     }
+    if (rinv && threadIdx.x == 0) rinv[t] = r;
     float xn[CPT][8];
     float m = 0.0f;
 #pragma unroll
@@ -718,7 +728,7 @@ static int pick_cpt(int64_t nchunk, const int *list, int n, int max_threads, int
     return 0;
 }
 
-constexpr int kRmsCpt[] = {1, 2, 3, 4, 6, 8};   // larger CPT spills registers; 8 of 512 threads hold rows of 32768
+constexpr int kRmsCpt[] = {1, 2, 3, 4, 6, 8};   // 8 of 512 threads hold rows of 32768
 constexpr int kSwiCpt[] = {1, 2, 3, 4, 6, 8};
 
 template <int CPT, bool ADD>
@@ -740,11 +750,11 @@ static cudaError_t rms_launch(const void *X, const void *R, void *H, const float
     if (!(reinterpret_cast<uintptr_t>(w) & 15u)) {
         // What a thread does whatever its share (both reductions, the root and two divisions) costs about as much as two
         // chunks, so many rows take few threads each; where all rows are in flight at once a row's latency counts and
-        // it takes more.  Up to four chunks a thread while 512 threads do (six spill).  Measured (us, up to 128 / 256 /
-        // 512 threads): 1 x 2560 2.8 / 2.5 / 2.3, 2048 x 3200 14.5 / 12.9 / 15.6, 16381 x 4096 85.9 / 91.2 / 116,
-        // 6000 x 8640 (six chunks with 128 and 256) 98.6 / 98.6 / 79.6.
+        // it takes more.  Up to six chunks a thread while 512 threads do.  Measured with a residual (us, up to 128 / 256 /
+        // 512 threads): 1 x 2560 2.6 / 2.3 / 2.1, 2048 x 3200 12.1 / 11.7 / 15.5, 16381 x 4096 76.9 / 76.7 / 119 (without
+        // one 50 / 62 / 102), 6000 x 8640 (six chunks with 256, three with 512) - / 60.1 / 62.0.
         int most = T <= 2 * num_sms() ? 512 : T <= 16 * num_sms() ? 256 : 128;
-        while (most < 512 && K / 8 > 4 * most) most *= 2;
+        while (most < 512 && K / 8 > 6 * most) most *= 2;
         cpt = pick_cpt(K / 8, kRmsCpt, 6, most, &threads);
     }
     if (cpt == 0) {   // rows beyond the register cache, or a weight vector without 16-byte alignment
