@@ -340,6 +340,9 @@ bitnet_status bitnet_adamw_step_batch(const bitnet_adamw_item *items, int32_t n_
  *   eps_norm > 0 (added to the mean square);  eps_act > 0 (absmax floor).
  *   Xq       [T, K] int8 out, 16-byte aligned.  absmax [T] fp32 out (= a[t]).
  *   rinv     [T] fp32 out (= r) or NULL.
+ * A row that holds Inf or NaN gets absmax NaN, codes 0 and r = 0 (Inf) or NaN;
+ * so does absmax, with codes 0, where w makes a value Inf or NaN.  A mean square
+ * above the fp32 range is Inf: r = 0, codes 0, absmax eps_act.
  * Errors: INVALID_ARG, UNSUPPORTED (T >= 2^31), CUDA.
  * ------------------------------------------------------------------------ */
 bitnet_status bitnet_rmsnorm_quant(const void *X, const float *w, int64_t T, int64_t K, float eps_norm,

@@ -152,6 +152,12 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
+// the largest magnitude of m, a and b, NaN where one is
+__device__ __forceinline__ float max_abs_or_nan(float m, float a, float b) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+    return d;
+}
 template <bool OR_NAN>
 __device__ __forceinline__ float larger(float a, float b) {
     return OR_NAN ? max_or_nan(a, b) : fmaxf(a, b);
@@ -423,15 +429,16 @@ __device__ __forceinline__ uint2 codes8(const float *v, float s) {
 }
 
 // block max (s_red: one float per warp); one call per kernel
+template <bool OR_NAN = false>
 __device__ __forceinline__ float rc_block_max(float v, float *s_red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = larger<OR_NAN>(v, __shfl_xor_sync(0xffffffffu, v, o));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     if (lane == 0) s_red[warp] = v;
     __syncthreads();
     float r = lane < nw ? s_red[lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+    for (int o = 16; o > 0; o >>= 1) r = larger<OR_NAN>(r, __shfl_xor_sync(0xffffffffu, r, o));
     return r;   // every warp reduces the same values: no second barrier needed
 }
 
@@ -540,8 +547,8 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // S by fp64 fused multiply-adds.  At most 64 of them per thread, 5 steps in a warp and 16 over the warps: the sum is
     // within 2^-46 of the exact one, and so are 1/K and the product.  Where everything within 2^-44 of the quotient
-    // rounds to the same fp32 (all but one row in 2^19), that is ms; else, and for tiny rows (zeros and subnormals are
-    // taken as about 2^-127 here), the exact sum decides.
+    // rounds to the same fp32 (all but one row in 2^19), that is ms; else the exact sum decides, and for tiny rows (zeros and
+    // subnormals are taken as about 2^-127 here) and an ms of Inf (Inf and NaN are taken as about 2^128).
     double sq = 0.0;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
     for (int i = 1; i < nw; ++i) sq += s_sq[i];
     const double q = sq * inv_k;
     const float ms = __double2float_rn(q * (1.0 - 0x1p-44));
-    const bool sure = q > 0x1p-120 && ms == __double2float_rn(q * (1.0 + 0x1p-44));   // the same for every thread
+    const bool sure = q > 0x1p-120 && ms < INFINITY && ms == __double2float_rn(q * (1.0 + 0x1p-44));   // the same for every thread
     float r;
     if (sure) {
         r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps_n)));
@@ -594,13 +601,17 @@ __global__ void __launch_bounds__(512) k_rmsnorm_quant_rc(const uint4 *X, const 
             for (int e = 0; e < 8; ++e) xn[j][e] = __fmul_rn(xn[j][e], r);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(xn[j][e]));
+        for (int e = 0; e < 8; e += 2) m = max_abs_or_nan(m, xn[j][e], xn[j][e + 1]);
     }
-    m = rc_block_max(m, s_red);
-    const float a = m > eps_a ? m : eps_a;
+    m = rc_block_max<true>(m, s_red);
+    const float a = m <= eps_a ? eps_a : m;   // NaN stays NaN
     const float s = __fdiv_rn(127.0f, a);
     if (threadIdx.x == 0) amax[t] = a;
     uint2 *out = reinterpret_cast<uint2 *>(Xq + t * K);
+    if (!(a < INFINITY)) {   // no scale: the codes are 0
+        for (int c = threadIdx.x; c < nchunk; c += blockDim.x) out[c] = make_uint2(0u, 0u);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
         const int c = threadIdx.x + j * blockDim.x;

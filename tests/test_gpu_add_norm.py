@@ -194,3 +194,13 @@ def _not_finite(bn, T, K, weighted, off, fused):
 @pytest.mark.parametrize("fused", [True, False])
 def test_rows_that_are_not_finite_in_the_general_form(bn, K, weighted, off, fused):
     _not_finite(bn, 9, K, weighted, off, fused)
+
+
+@pytest.mark.parametrize("K,weighted", [(8 * 3 + 8, False), (264, True), (2560, True), (3200, False), (8640, True), (16384, False),
+                                        (32768, True)])
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("T", [9, 2500])
+def test_rows_that_are_not_finite(bn, T, K, weighted, fused):
+    if T * K > 10 ** 7:
+        pytest.skip("the number of rows changes the threads per row only")
+    _not_finite(bn, T, K, weighted, False, fused)
