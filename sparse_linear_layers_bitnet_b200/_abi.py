@@ -231,12 +231,27 @@ def _new(shape, dtype, like, stream):
 
 def _ws(ws, size, like, stream):
     """(tensor that holds it, address, bytes) of the workspace ws, or of one for this call
-    (whose status word nobody reads) of size() bytes."""
+    (contents uninitialised) of size() bytes."""
     if ws is not None:
         assert ws.buf.get_device() == like.get_device()
         return ws.buf, ws.buf.data_ptr(), ws.nbytes
     buf = _new((max(size(), 256),), _torch().uint8, like, stream)
     return buf, buf.data_ptr(), buf.numel()
+
+
+def _launch_checked(name: str, index: int, ws, size, like, stream, *args) -> None:
+    """_launch with a workspace behind args.  The caller's ws keeps the status word for the caller to read; without one
+    the call waits for its kernels and raises BitnetError where an index on the device was out of range."""
+    keep, ptr, nbytes = _ws(ws, size, like, stream)
+    if ws is not None:
+        return _launch(name, index, stream, *args, ptr, nbytes)
+    torch = _torch()
+    with torch.cuda.device(index), torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(index)):
+        if torch.cuda.is_current_stream_capturing():
+            raise BitnetError(BITNET_ERR_WORKSPACE, name, "a captured call needs a workspace whose status can be read after a replay")
+        keep[:256].zero_()
+        _launch(name, index, None, *args, ptr, nbytes)
+        check(load().bitnet_read_device_status(ptr, torch.cuda.current_stream().cuda_stream), name)
 
 
 def _ld(t) -> int:
@@ -611,7 +626,9 @@ def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interl
                 inverse: bool = False, Y=None, ws: "Workspace | None" = None, stream=None):
     """Rotary positions pos (int32 [T]) on the first n_heads heads of the rows of X (fp32 or bf16
     [T, >= n_heads * head_dim], rows may be strided); table as rope_table makes it.  inverse: the
-    gradient.  Y may be X.  Returns Y."""
+    gradient.  Y may be X.  Rows of a negative position are left as they were (a new Y: uninitialised), and so
+    are those of a position behind the table, which ws reports (bitnet_read_device_status); without ws the call
+    waits for its kernels and raises BitnetError for one.  Returns Y."""
     torch = _torch()
     assert X.dim() == 2 and X.dtype in (torch.float32, torch.bfloat16) and X.is_cuda and (X.shape[1] == 0 or X.stride(1) == 1)
     T = X.shape[0]
@@ -625,10 +642,9 @@ def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interl
         Y = _new((T, n_heads * head_dim), X.dtype, X, stream)
     assert Y.dim() == 2 and Y.dtype == X.dtype and Y.get_device() == index and Y.stride(1) == 1
     assert Y.shape[0] == T and Y.shape[1] >= n_heads * head_dim
-    keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, X, stream)
-    _launch("bitnet_rope", index, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(), table.data_ptr(), n_pos,
-            T, n_heads, head_dim, 2 * half, 1 if interleaved else 0, 1 if inverse else 0, Y.data_ptr(), _ld(Y), ws_ptr,
-            ws_bytes)
+    _launch_checked("bitnet_rope", index, ws, lambda: 256, X, stream, X.data_ptr(), _dtype_code(X.dtype), _ld(X), pos.data_ptr(),
+                    table.data_ptr(), n_pos, T, n_heads, head_dim, 2 * half, 1 if interleaved else 0, 1 if inverse else 0,
+                    Y.data_ptr(), _ld(Y))
     return Y
 
 
@@ -637,7 +653,9 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
     """Rotary positions on the query and key heads of QKV (fp32 or bf16 [T, (heads + 2 kv heads) * head_dim],
     rows may be strided); keys and values go to the cache K, V (bf16 [pages, kv heads, page, head_dim], any
     strides with contiguous rows), row pos of sequence seq (default: row t is sequence t) by its page list in
-    pages (int32 [sequences, most pages]).  table None: no rotation.  Returns Q (bf16 [T, heads * head_dim])."""
+    pages (int32 [sequences, most pages]).  table None: no rotation.  Nothing is written for rows of a negative
+    pos or seq (a new Q: uninitialised there), nor for those of an index out of range, which ws reports; without
+    ws the call waits for its kernels and raises BitnetError for one.  Returns Q (bf16 [T, heads * head_dim])."""
     torch = _torch()
     c = _cache_struct(K, V)
     assert QKV.dim() == 2 and QKV.dtype in (torch.float32, torch.bfloat16) and QKV.stride(1) == 1
@@ -653,10 +671,9 @@ def bitnet_rope_append(QKV, pos, table, K, V, pages, seq=None, interleaved: bool
     assert table is None or _is(table, torch.float32, (n_pos, half, 2), index)
     Q = _new((T, heads * c.head_dim), torch.bfloat16, QKV, stream) if Q is None else Q
     assert _is(Q, torch.bfloat16, (T, heads * c.head_dim), index)
-    keep, ws_ptr, ws_bytes = _ws(ws, lambda: 256, QKV, stream)
-    _launch("bitnet_rope_append", index, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV), pos.data_ptr(), _addr(seq),
-            _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0, ctypes.byref(c), pages.data_ptr(), n_seqs,
-            max_pages, Q.data_ptr(), ws_ptr, ws_bytes)
+    _launch_checked("bitnet_rope_append", index, ws, lambda: 256, QKV, stream, QKV.data_ptr(), _dtype_code(QKV.dtype), _ld(QKV),
+                    pos.data_ptr(), _addr(seq), _addr(table), n_pos, T, heads, 2 * half, 1 if interleaved else 0,
+                    ctypes.byref(c), pages.data_ptr(), n_seqs, max_pages, Q.data_ptr())
     return Q
 
 
@@ -665,7 +682,8 @@ def bitnet_paged_attn(Q, K, V, pages, lens, scale: float | None = None, O=None, 
     """Attention of one token per sequence: Q bf16 [sequences, heads * head_dim] (rows may be strided) over the
     first lens (int32 [sequences]) keys of each sequence in the cache K, V by its page list in pages (see
     bitnet_rope_append).  scale: head_dim^-1/2 unless given.  lse: fp32 [sequences, heads], filled when given.
-    Returns O (bf16 unless o_dtype says fp32)."""
+    A length or page out of range is reported by ws; without ws the call waits for its kernels and raises
+    BitnetError for one.  Returns O (bf16 unless o_dtype says fp32)."""
     torch = _torch()
     c = _cache_struct(K, V)
     index = K.get_device()
@@ -679,11 +697,10 @@ def bitnet_paged_attn(Q, K, V, pages, lens, scale: float | None = None, O=None, 
         O = _new((n_seqs, width), torch.bfloat16 if o_dtype is None else o_dtype, Q, stream)
     assert O.shape == Q.shape and O.stride(1) == 1 and O.get_device() == index and (o_dtype is None or O.dtype == o_dtype)
     assert lse is None or _is(lse, torch.float32, (n_seqs, heads), index)
-    keep, ws_ptr, ws_bytes = _ws(
-        ws, lambda: load().bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream)
-    _launch("bitnet_paged_attn", index, stream, Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(),
-            max_pages, lens.data_ptr(), c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(),
-            _dtype_code(O.dtype), _ld(O), _addr(lse), ws_ptr, ws_bytes)
+    _launch_checked("bitnet_paged_attn", index, ws,
+                    lambda: load().bitnet_paged_attn_workspace_size(n_seqs, heads, c.n_kv_heads, c.head_dim), Q, stream,
+                    Q.data_ptr(), _ld(Q), n_seqs, heads, ctypes.byref(c), pages.data_ptr(), max_pages, lens.data_ptr(),
+                    c.head_dim ** -0.5 if scale is None else scale, O.data_ptr(), _dtype_code(O.dtype), _ld(O), _addr(lse))
     return O
 
 

@@ -307,3 +307,47 @@ def test_rope_of_many_rows_in_place(bn, d, rot, heads, dtype):
     xd = up(x, dtype)
     bn.bitnet_rope(xd, up(pos, torch.int32), up(tab), heads, Y=xd)
     assert np.array_equal(host(xd).view(np.uint32), ref.view(np.uint32))
+
+
+def test_without_a_workspace_a_bad_index_raises(bn):
+    """Nobody could read the status word of a workspace that the call made for itself."""
+    x, tab = torch.randn(4, 128, device="cuda"), up(table_ref(16, 64))
+    fine = up(np.array([0, 15, -5, 3], np.int32), torch.int32)
+    bn.bitnet_rope(x, fine, tab, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    bad = up(np.array([0, 16, -5, 3], np.int32), torch.int32)
+    torch.cuda.synchronize()
+    for stream in (None, s):
+        with pytest.raises(bn.BitnetError, match="out of range"):
+            bn.bitnet_rope(x, bad, tab, 2, stream=stream)
+    K, V = bn.kv_cache(4, 1, 16, 64), bn.kv_cache(4, 1, 16, 64)
+    qkv = torch.randn(2, 4 * 64, device="cuda").to(BF16)
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pages = up(np.array([[0], [4]], np.int32), torch.int32)          # page 4 of four
+    with pytest.raises(bn.BitnetError, match="out of range"):
+        bn.bitnet_rope_append(qkv, pos, tab, K, V, pages)
+    with pytest.raises(bn.BitnetError, match="out of range"):
+        bn.bitnet_paged_attn(qkv[:, :64].contiguous(), K, V, pages, pos + 1)
+    pages.zero_()
+    q = bn.bitnet_rope_append(qkv[:1], pos[:1], tab, K, V, pages[:1])
+    bn.bitnet_paged_attn(q, K, V, pages[:1], pos[:1] + 1)
+    assert bn.bitnet_rope(x[:0], fine[:0], tab, 2).shape == (0, 128)
+
+
+def test_a_captured_call_needs_a_workspace(bn):
+    x, tab = torch.randn(4, 128, device="cuda"), up(table_ref(16, 64))
+    pos, y, ws = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.empty(4, 128, device="cuda"), bn.Workspace(256)
+    bn.bitnet_rope(x, pos, tab, 2, Y=y, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bn.bitnet_rope(x, pos, tab, 2, Y=y, ws=ws)
+        with pytest.raises(bn.BitnetError, match="workspace"):
+            bn.bitnet_rope(x, pos, tab, 2, Y=y)
+    pos.fill_(16)
+    g.replay()
+    assert bn.bitnet_read_device_status(ws) == bn._abi.BITNET_ERR_INVALID_ARG
+    pos.fill_(0)
+    g.replay()
+    assert bn.bitnet_read_device_status(ws) == 0 and torch.equal(y, x)
