@@ -625,15 +625,17 @@ def _cache_struct(K, V) -> BitnetKvCache:
 def bitnet_rope(X, pos, table, n_heads: int, head_dim: int | None = None, interleaved: bool = False,
                 inverse: bool = False, Y=None, ws: "Workspace | None" = None, stream=None):
     """Rotary positions pos (int32 [T]) on the first n_heads heads of the rows of X (fp32 or bf16
-    [T, >= n_heads * head_dim], rows may be strided); table as rope_table makes it.  inverse: the
-    gradient.  Y may be X.  Rows of a negative position are left as they were (a new Y: uninitialised), and so
-    are those of a position behind the table, which ws reports (bitnet_read_device_status); without ws the call
-    waits for its kernels and raises BitnetError for one.  Returns Y."""
+    [T, >= n_heads * head_dim], rows may be strided); table as rope_table makes it.  Without head_dim the rows
+    must hold the n_heads heads and nothing behind them, so a QKV row needs it.  inverse: the gradient.  Y may be
+    X.  Rows of a negative position are left as they were (a new Y: uninitialised), and so are those of a
+    position behind the table, which ws reports (bitnet_read_device_status); without ws the call waits for its
+    kernels and raises BitnetError for one.  Returns Y."""
     torch = _torch()
     assert X.dim() == 2 and X.dtype in (torch.float32, torch.bfloat16) and X.is_cuda and (X.shape[1] == 0 or X.stride(1) == 1)
     T = X.shape[0]
-    if head_dim is None:
+    if head_dim is None:   # the rows are these heads and nothing else
         head_dim = X.shape[1] // n_heads
+        assert X.shape[1] == n_heads * head_dim, "rows that hold more than n_heads heads need head_dim"
     assert X.shape[1] >= n_heads * head_dim
     index = X.get_device()
     n_pos, half, _ = table.shape

@@ -351,3 +351,13 @@ def test_a_captured_call_needs_a_workspace(bn):
     pos.fill_(0)
     g.replay()
     assert bn.bitnet_read_device_status(ws) == 0 and torch.equal(y, x)
+
+
+def test_rows_of_more_than_the_heads_need_head_dim(bn):
+    """Five heads of 64 and two more behind them: 448 / 5 is no head's size."""
+    x, tab = torch.randn(3, 448, device="cuda"), up(table_ref(16, 64))
+    pos = torch.ones(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(AssertionError, match="head_dim"):
+        bn.bitnet_rope(x, pos, tab, 5)
+    y = bn.bitnet_rope(x, pos, tab, 5, 64)
+    assert y.shape == (3, 320) and torch.equal(y, bn.bitnet_rope(x[:, :320].contiguous(), pos, tab, 5))
