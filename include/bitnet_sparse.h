@@ -392,7 +392,8 @@ bitnet_status bitnet_add_rmsnorm_quant(const void *X, const void *R, const float
  *   dw        [K] fp32 out or NULL; accumulate != 0 adds to it (gradient
  *             accumulation), else it is overwritten (T = 0: zeros).
  *   ws        >= bitnet_rmsnorm_grad_workspace_size(T, K) bytes, 16-byte aligned,
- *             contents ignored; may be NULL when dw is NULL.
+ *             contents ignored; may be NULL when dw is NULL.  Calls that may run at
+ *             the same time need workspaces of their own.
  * dY, H, w, dR and dH 16-byte aligned; K % 8 == 0, K <= 65536.
  * Errors: INVALID_ARG, UNSUPPORTED (T >= 2^31), WORKSPACE, CUDA.
  * ------------------------------------------------------------------------ */

@@ -543,10 +543,11 @@ def bitnet_add_rmsnorm_quant(X, R, w=None, eps_norm: float = 1e-6, eps_act: floa
 
 
 def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumulate: bool = False,
-                        ws: "Workspace | None" = None, stream=None):
+                        ws: "Workspace | None" = None, stream=None, need_dw: bool = True):
     """Gradient of RMSNorm at its rows H (bf16 [T, K], rinv as the forward wrote it) for the gradient dY
     (fp32 or bf16) of the normalised values; dR: the residual stream's own gradient, added to dH.
-    Returns (dH, dw): dH of dR's (or dH's own) type, bf16 unless given; dw fp32."""
+    Returns (dH, dw): dH of dR's (or dH's own) type, bf16 unless given; dw fp32, or None with need_dw False (a
+    frozen or absent weight: the launch that sums it, and the workspace, fall away)."""
     torch = _torch()
     T, K = H.shape
     f32, rows, index = torch.float32, (T, K), H.get_device()
@@ -555,12 +556,18 @@ def bitnet_rmsnorm_grad(dY, H, rinv, w=None, dR=None, dH=None, dw=None, accumula
     assert w is None or _is(w, f32, (K,), index)
     g = dH.dtype if dH is not None else dR.dtype if dR is not None else torch.bfloat16
     dH = _new((T, K), g, H, stream) if dH is None else dH
-    dw = _new((K,), torch.float32, H, stream) if dw is None else dw
     assert dR is None or _is(dR, g, rows, index)
-    assert _is(dH, g, rows, index) and _is(dw, f32, (K,), index)
-    keep, ws_ptr, ws_bytes = _ws(ws, lambda: load().bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
+    assert _is(dH, g, rows, index)
+    keep = ws_ptr = None
+    ws_bytes = 0
+    if need_dw:
+        dw = _new((K,), torch.float32, H, stream) if dw is None else dw
+        assert _is(dw, f32, (K,), index)
+        keep, ws_ptr, ws_bytes = _ws(ws, lambda: load().bitnet_rmsnorm_grad_workspace_size(T, K), H, stream)
+    else:
+        assert dw is None
     _launch("bitnet_rmsnorm_grad", index, stream, dY.data_ptr(), _dtype_code(dY.dtype), H.data_ptr(), _addr(w),
-            rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
+            rinv.data_ptr(), _addr(dR), _dtype_code(g), T, K, dH.data_ptr(), _addr(dw), 1 if accumulate else 0,
             ws_ptr, ws_bytes)
     return dH, dw
 

@@ -169,3 +169,20 @@ def test_refusals(bn):
         bn.bitnet_rmsnorm_grad(H.clone(), H, r, dH=H)
     with pytest.raises(bn.BitnetError):
         bn.bitnet_rmsnorm_grad(H.clone(), H, r, ws=bn.Workspace(256))
+
+
+@pytest.mark.parametrize("T,K", [(40, 3200), (300, 12288), (300, 12296)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_without_the_weight_gradient(bn, T, K, residual):
+    """The longest row of the register form and the shortest beyond it: dH is the same with dw and without."""
+    dY, H, rinv, w, dR = inputs(T, K, torch.float32, torch.bfloat16, True, residual, K)
+    a = (dev(dY, torch.float32), dev(H, torch.bfloat16), dev(rinv, torch.float32))
+    kw = dict(w=dev(w, torch.float32), dR=dev(dR, torch.bfloat16) if residual else None)
+    dH, dw = bn.bitnet_rmsnorm_grad(*a, **kw)
+    alone, none = bn.bitnet_rmsnorm_grad(*a, **kw, need_dw=False)
+    assert none is None and torch.equal(alone, dH)
+    ref, bound, dw_ref, dw_bound = formula(dY, H, rinv, w, dR)
+    check(dH, ref, bound, torch.bfloat16)
+    check(dw, dw_ref, dw_bound, torch.float32)
+    with pytest.raises(AssertionError):
+        bn.bitnet_rmsnorm_grad(*a, **kw, dw=dw, need_dw=False)
