@@ -169,3 +169,50 @@ def test_training_step(bn):
     ref, bound, dw_ref, dw_bound = formula(host(dy), host(h), host(rinv), host(blk.w1), host(up_grad))
     assert np.all(np.abs(host(dh) - ref) <= bound + 2.0 ** -8 * (np.abs(ref) + bound))
     assert np.all(np.abs(host(dw) - dw_ref) <= dw_bound)
+
+
+@pytest.mark.parametrize("B", [1, 8, 33])
+def test_captured_decode_steps_write_the_cache(bn, B):
+    """Four steps one by one, and the same captured and replayed on a cache that holds NaN behind what the sequences held
+    at the start: every replay has to write its own keys and values before it reads them."""
+    r = np.random.default_rng(100 + B)
+    start = r.integers(0, 40, B)
+    blk = Block(bn, B, seed=B)
+    blk.K.fill_(float("nan")), blk.V.fill_(float("nan"))
+    for b in range(B):
+        n = int(start[b])
+        if n:
+            qkv = up(r.normal(size=(n, (HEADS + 2 * KV) * D)).astype(np.float32), BF16)
+            bn.bitnet_rope_append(qkv, up(np.arange(n), torch.int32), blk.table, blk.K, blk.V, blk.pages,
+                                  seq=torch.full((n,), b, dtype=torch.int32, device="cuda"), ws=blk.ws)
+    first = [t.clone() for t in (blk.K, blk.V)]
+    pos, lens = up(start, torch.int32), up(start + 1, torch.int32)
+    x0, d0 = (up(r.normal(size=(B, HID)).astype(np.float32), BF16) for _ in range(2))
+    x, delta, made = x0, d0, []
+    for _ in range(4):
+        s = blk.step(x, delta, pos, lens)
+        x, delta = s["h2"], s["out"]
+        assert not bool(torch.isnan(x.float()).any() or torch.isnan(delta.float()).any())
+        made.append((x.clone(), delta.clone()))
+        pos.add_(1), lens.add_(1)
+    last = [t.clone() for t in (blk.K, blk.V)]
+    assert int(torch.isnan(first[0].float()).sum() - torch.isnan(last[0].float()).sum()) == 4 * B * KV * D
+
+    gx, gd = x0.clone(), d0.clone()
+    pos, lens = up(start, torch.int32), up(start + 1, torch.int32)
+    blk.step(gx, gd, pos, lens)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = blk.step(gx, gd, pos, lens)
+        gx.copy_(s["h2"]), gd.copy_(s["out"])
+        pos.add_(1), lens.add_(1)
+    blk.K.copy_(first[0]), blk.V.copy_(first[1])
+    gx.copy_(x0), gd.copy_(d0)
+    pos.copy_(up(start, torch.int32)), lens.copy_(up(start + 1, torch.int32))
+    for x, delta in made:
+        g.replay()
+        assert torch.equal(gx, x) and torch.equal(gd, delta)
+    for got, want in zip((blk.K, blk.V), last):
+        assert torch.equal(torch.nan_to_num(got, nan=3.0), torch.nan_to_num(want, nan=3.0))
+    assert bn.bitnet_read_device_status(blk.ws) == 0
