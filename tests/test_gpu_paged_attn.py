@@ -378,3 +378,18 @@ def test_infinities_and_nan_in_keys_and_values(bn, heads, kv, d, dtype):
     bound = 2 * (2.0 ** -17 + 2.0 ** -20) * size
     bound += (2.0 ** -8 if dtype == BF16 else U) * (np.abs(np.where(ok, ref, 0)) + bound)
     assert np.all(np.abs(got[ok] - ref[ok]) <= bound[ok])
+
+
+@pytest.mark.parametrize("n,heads,d", [(60000, 5, 128), (45000, 16, 100), (45000, 3, 256)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_head_over_more_ranges_than_a_join_takes_at_once(bn, n, heads, d, dtype):
+    """One sequence and one key-value head cut over more than 128 ranges: the join's warps take their partials in several
+    rounds, and the largest scores come near the end, so that what they have is rescaled."""
+    c = Case([n], heads, 1, d, 64, seed=n + d)
+    late = int(0.97 * n)
+    for j in range(late, late + 3):
+        c.k[0][0, j] = c.q[0, :d]
+    for j in range(-(-n // 64)):
+        rows = slice(64 * j, min(n, 64 * j + 64))
+        c.K[c.pages[0, j], :, :rows.stop - rows.start].copy_(up(c.k[0][:, rows], BF16))
+    check_case(bn, c, dtype)
