@@ -361,3 +361,41 @@ def test_rows_of_more_than_the_heads_need_head_dim(bn):
         bn.bitnet_rope(x, pos, tab, 5)
     y = bn.bitnet_rope(x, pos, tab, 5, 64)
     assert y.shape == (3, 320) and torch.equal(y, bn.bitnet_rope(x[:, :320].contiguous(), pos, tab, 5))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T", [21, 1500])
+def test_odd_row_strides_and_a_table_off_16_bytes(bn, dtype, interleaved, T):
+    """Rows an odd number of elements apart that start off the vectors' alignment, a table on 8 bytes only."""
+    heads, d, rot, n_pos = 5, 64, 48, 300
+    r = np.random.default_rng(T)
+    x = r.normal(size=(T, heads * d)).astype(np.float32)
+    x = bf16(x) if dtype == BF16 else x
+    pos = r.integers(0, n_pos, T).astype(np.int32)
+    tab = table_ref(n_pos, rot)
+    flat = torch.zeros(2 + tab.size, device="cuda")
+    flat[2:] = up(tab).reshape(-1)
+    td = flat[2:].view(n_pos, rot // 2, 2)
+    assert td.data_ptr() % 16 == 8
+    ref = turn(x.reshape(T, heads, d), tab[pos], interleaved).reshape(T, -1)
+    ref = bf16(ref) if dtype == BF16 else ref
+    aligned = up(x, dtype)
+    assert np.array_equal(host(bn.bitnet_rope(aligned, up(pos, torch.int32), td, heads, interleaved=interleaved)).view(np.uint32), ref.view(np.uint32))
+    wide, out = (torch.full((T, heads * d + 7), 9.0, dtype=dtype, device="cuda") for _ in range(2))
+    xv, yv = wide[:, 3:3 + heads * d], out[:, 1:1 + heads * d]
+    xv.copy_(aligned)
+    bn.bitnet_rope(xv, up(pos, torch.int32), td, heads, d, interleaved=interleaved, Y=yv)
+    assert np.array_equal(host(yv).view(np.uint32), ref.view(np.uint32))
+    assert bool((out[:, 0] == 9.0).all()) and bool((out[:, 1 + heads * d:] == 9.0).all())
+    bn.bitnet_rope(xv, up(pos, torch.int32), td, heads, d, interleaved=interleaved, Y=xv)      # in place
+    assert np.array_equal(host(xv).view(np.uint32), ref.view(np.uint32))
+    K, V = bn.kv_cache(-(-T // 16), 1, 16, d), bn.kv_cache(-(-T // 16), 1, 16, d)
+    xv.copy_(aligned)                                                 # three query heads, a key and a value head
+    Q = bn.bitnet_rope_append(xv, up(np.arange(T) % n_pos if T < n_pos else np.arange(T), torch.int32), td if T < n_pos else None,
+                              K, V, torch.arange(-(-T // 16), dtype=torch.int32, device="cuda")[None].contiguous(),
+                              seq=torch.zeros(T, dtype=torch.int32, device="cuda"), interleaved=interleaved)
+    h = x.reshape(T, heads, d)
+    qk = turn(h[:, :4], tab[np.arange(T)], interleaved) if T < n_pos else h[:, :4]
+    assert np.array_equal(host(Q), bf16(qk[:, :3]).reshape(T, -1))
+    assert np.array_equal(host(K)[:, 0].reshape(-1, d)[:T], bf16(qk[:, 3])) and np.array_equal(host(V)[:, 0].reshape(-1, d)[:T], bf16(h[:, 4]))
