@@ -19,6 +19,10 @@
  *   - No C++ exception crosses this boundary.
  *   - A call with T == 0 (empty batch) validates its sizes, launches nothing,
  *     and accepts NULL activation / output buffers.
+ *   - Where a workspace holds the device status word (its first 4 bytes), the
+ *     kernels only set bits in it, so it has to be zero before its first use:
+ *     zero the buffer, or call bitnet_read_device_status once, which clears it.
+ *     What lies behind it may hold anything.
  *   - bitnet_last_error() returns a human-readable detail of the last failure
  *     on the calling thread.
  */
@@ -427,8 +431,9 @@ bitnet_status bitnet_rmsnorm_grad(const void *dY, bitnet_dtype dy_dtype, const v
  *             BITNET_ROPE_INTERLEAVED: pair i is (x_{2i}, x_{2i+1}).
  *   Y         [T, ldy] of the same type; may be X itself with ldy == ldx.
  *   ws        >= bitnet_rope_workspace_size() bytes, 16-byte aligned: the status
- *             word.  A position >= n_pos sets it (bitnet_read_device_status
- *             returns INVALID_ARG) and leaves that row of Y as it was.
+ *             word, zero before its first use.  A position >= n_pos sets it
+ *             (bitnet_read_device_status returns INVALID_ARG) and leaves that
+ *             row of Y as it was.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------ */
 enum { BITNET_ROPE_HALVES = 0, BITNET_ROPE_INTERLEAVED = 1 };
@@ -513,8 +518,9 @@ bitnet_status bitnet_rope_append(const void *QKV, bitnet_dtype dtype, int64_t ld
  *   O         [n_seqs, ldo] of o_dtype; must not overlap Q.   lse  [n_seqs,
  *             n_heads] fp32 or NULL.
  *   ws        >= bitnet_paged_attn_workspace_size(...) bytes, 16-byte aligned:
- *             status word and partial results (contents ignored).  Calls that
- *             may run at the same time need workspaces of their own.
+ *             status word (zero before its first use) and partial results
+ *             (contents ignored).  Calls that may run at the same time need
+ *             workspaces of their own.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------ */
 size_t bitnet_paged_attn_workspace_size(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);

@@ -399,3 +399,12 @@ def test_odd_row_strides_and_a_table_off_16_bytes(bn, dtype, interleaved, T):
     qk = turn(h[:, :4], tab[np.arange(T)], interleaved) if T < n_pos else h[:, :4]
     assert np.array_equal(host(Q), bf16(qk[:, :3]).reshape(T, -1))
     assert np.array_equal(host(K)[:, 0].reshape(-1, d)[:T], bf16(qk[:, 3])) and np.array_equal(host(V)[:, 0].reshape(-1, d)[:T], bf16(h[:, 4]))
+
+
+def test_a_workspace_that_held_anything_is_cleared_by_a_read(bn):
+    x, tab = torch.randn(4, 128, device="cuda"), up(table_ref(16, 64))
+    pos, ws = torch.zeros(4, dtype=torch.int32, device="cuda"), bn.Workspace(256)
+    ws.buf.fill_(255)
+    assert bn.bitnet_read_device_status(ws) != 0
+    bn.bitnet_rope(x, pos, tab, 2, ws=ws)
+    assert bn.bitnet_read_device_status(ws) == 0
