@@ -6,13 +6,14 @@
 //   dh_k = r (e_k - u_k (1/K) sum_j e_j u_j) + dR_k,   dw_k = sum_t g_k u_k.
 // r is the forward's (rinv).  All sums are fp32; dh is rounded once.
 //
-// Every byte is touched once: a CTA takes whole rows (its threads hold the
+// Rows of up to 12288 are touched once: a CTA takes whole rows (its threads hold the
 // row's 16-byte chunks in registers between the dot product and the result)
 // and walks over rows blockIdx.x, + gridDim.x, ..., keeping its columns' dw in
 // registers.  A second launch adds the CTAs' dw rows in a fixed order, so dw
 // does not depend on timing.  Bound: HBM for many rows (8191 x 4096 with an fp32
-// dY 49 us, 5.5 TB/s); 2048 x 3200 with a residual branch takes 16.4 us, about 3
-// of them the second launch.
+// dY 47 us, 5.7 TB/s); 2048 x 3200 with a residual branch takes 15.3 us, about 3
+// of them the second launch.  Longer rows are read twice, and a third time for
+// dw: 4096 x 16384 with a residual branch 173 us, a floor of 82 (4096 x 12288: 86, 62).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -94,8 +95,11 @@ __global__ void __launch_bounds__(THREADS) k_rmsnorm_grad(const TY *__restrict__
     for (int j = 0; j < CPT; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-    // the next row is on its way while this one is worked on (with up to two chunks a thread: more do not fit the registers)
-    constexpr bool kAhead = CPT <= 2;
+    // The next row is on its way while this one is worked on, where its words leave the registers room: two chunks with a
+    // 16-bit side spill up to 60 bytes and gain all the same, with both sides in fp32 they spill 128 and lose, three chunks
+    // lose throughout (4096 rows, without / with, us: 8640 bf16 72.7 / 55.9, fp32 dY 70.8 / 65.8, both fp32 117 / 129;
+    // 12288 86 / 114, both fp32 155 / 207).
+    constexpr bool kAhead = CPT * (sizeof(TY) + sizeof(TG) + 2) <= 16;
     Raw8<TY> ny[CPT];
     Raw8<__nv_bfloat16> nh[CPT];
     Raw8<TG> nr[CPT];
