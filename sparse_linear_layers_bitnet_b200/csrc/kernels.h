@@ -134,7 +134,7 @@ cudaError_t launch_rope_append(const void *QKV, bool bf16, int64_t ld, const int
                                int64_t max_pages, void *Q, uint32_t *status, cudaStream_t s);
 
 // One-token attention over the paged cache (paged_attn.cu)
-constexpr int kAttnMaxCtas = 4;   // CTAs per SM at most (sizes the partials)
+constexpr int kAttnMaxCtas = 2;   // CTAs per SM: what registers and shared memory leave (sizes the partials)
 size_t paged_attn_ws_bytes(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
 cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_t n_heads, const KvCacheHost &c,
                               const int32_t *pages, int64_t max_pages, const int32_t *lens, float scale, void *O, bool o_bf16,

@@ -4,8 +4,10 @@
 // p_j = 2^(x_j - m), x_j = (q . k_j) scale log2 e and m the largest x_j, in one
 // pass over the keys with a running m, sum and o (rescaled when m grows).
 //
-// Bound: HBM.  Every key and value is read once and used for the few query
-// heads that share it, a handful of operations per byte.  So:
+// Bound: HBM.  Every key and value is read once and used for the query heads
+// that share it, up to 16 of them (8 above 128 features), a handful of
+// operations per byte; more heads read it once for each 16 (8 x 16384 keys of one
+// head of 128: 16 query heads 29 us, 40 of them 45).  So:
 //  * The work of a call, in units of 128 keys of one key-value head, is cut into
 //    one equal contiguous range per CTA (whatever the lengths are; the end of a
 //    head counts as half a unit where there are many), and a CTA
@@ -1031,7 +1033,7 @@ cudaError_t launch_paged_attn(const void *Q, int64_t ldq, int64_t n_seqs, int64_
               : c.head_dim % 4 == 0 && ldq % 4 == 0 && (reinterpret_cast<uintptr_t>(Q) & 7) == 0 ? 8
                                                                                                  : 2;
     p.o_vec = c.head_dim % 4 == 0 && ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(O) & (o_bf16 ? 7 : 15)) == 0 ? 1 : 0;
-    // 32 keys at once and two to four CTAs per SM; at 256 features 16 keys, so that two CTAs fit
+    // 32 keys at once and two CTAs per SM; at 256 features 16 keys, so that two CTAs fit
     if (c.head_dim <= 64) return by_heads<1, 32, 4>(p, s);
     if (c.head_dim <= 128) return by_heads<2, 32, 3>(p, s);
     return by_heads<4, 16, 3>(p, s);
