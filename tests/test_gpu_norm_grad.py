@@ -71,7 +71,7 @@ def check(got, ref, bound, dtype):
     assert np.all(np.abs(got - ref) <= bound + 1e-37)
 
 
-# K: one chunk, every register width (1, 2 and 4 chunks a thread), ragged warps, and rows beyond them
+# K: one chunk, every register width (1, 2 and 3 chunks a thread), ragged warps, and rows beyond them
 @pytest.mark.parametrize("T,K", [(1, 8), (1, 2560), (3, 264), (700, 520), (33, 3200), (300, 4104), (13, 8192), (9, 8640), (7, 9240), (5, 16384),
                                  (301, 16392), (3, 65536)])
 @pytest.mark.parametrize("dy,g,weighted,residual", [(torch.bfloat16, torch.bfloat16, True, True),

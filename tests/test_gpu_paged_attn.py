@@ -393,3 +393,12 @@ def test_one_head_over_more_ranges_than_a_join_takes_at_once(bn, n, heads, d, dt
         rows = slice(64 * j, min(n, 64 * j + 64))
         c.K[c.pages[0, j], :, :rows.stop - rows.start].copy_(up(c.k[0][:, rows], BF16))
     check_case(bn, c, dtype)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
+@pytest.mark.parametrize("heads,kv,d", [(20, 5, 128), (7, 7, 100)])
+def test_scales(bn, scale, heads, kv, d):
+    """No scale at all (every key counts the same, what lies behind a length still nothing), a negative and a large one."""
+    c = Case(LENS, heads, kv, d, 16, seed=13)
+    c.scale = scale
+    check_case(bn, c, F32)
