@@ -7,7 +7,7 @@
 // Bound: HBM.  Every key and value is read once and used for the query heads
 // that share it, up to 16 of them (8 above 128 features), a handful of
 // operations per byte; more heads read it once for each 16 (8 x 16384 keys of one
-// head of 128: 16 query heads 29 us, 40 of them 45).  So:
+// head of 128: 16 query heads 31 us, 40 of them 47).  So:
 //  * The work of a call, in units of 128 keys of one key-value head, is cut into
 //    one equal contiguous range per CTA (whatever the lengths are; the end of a
 //    head counts as half a unit where there are many), and a CTA
@@ -38,10 +38,10 @@
 //    additions (7.6e-8 there; no cost but 3 to 4% with 16 query heads per
 //    key-value head).
 //
-// Measured: 8 contexts of 65536 to 131072 keys, 20 heads on 5 of 128 features,
-// 314 us (6.7 TB/s); 24 ragged sequences of up to 4096 keys x 32 heads of 100,
-// 101 us (5.5 TB/s); 128 sequences of up to 500 keys, 32 heads on 8, 31 us (4.2
-// TB/s: the ends of heads); one sequence of 4001 keys 8.6 us.
+// Measured on the device: 8 contexts of 65536 to 131072 keys, 20 heads on 5 of
+// 128 features, 312 us (6.7 TB/s); 24 ragged sequences of up to 4096 keys x 32
+// heads of 100, 100 us (5.6 TB/s); 128 sequences of up to 500 keys, 32 heads on
+// 8, 34 us (4.2 TB/s: the ends of heads); one sequence of 4001 keys 9.7 us.
 #include "common.cuh"
 #include "kernels.h"
 

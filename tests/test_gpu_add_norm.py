@@ -196,11 +196,9 @@ def test_rows_that_are_not_finite_in_the_general_form(bn, K, weighted, off, fuse
     _not_finite(bn, 9, K, weighted, off, fused)
 
 
-@pytest.mark.parametrize("K,weighted", [(8 * 3 + 8, False), (264, True), (2560, True), (3200, False), (8640, True), (16384, False),
-                                        (32768, True)])
+@pytest.mark.parametrize("T,K,weighted", [(9, 32, False), (9, 264, True), (9, 2560, True), (9, 3200, False), (9, 8640, True), (9, 16384, False),
+                                          (9, 32768, True), (2500, 32, False), (2500, 264, True), (2500, 2560, True), (2500, 3200, False)])
 @pytest.mark.parametrize("fused", [True, False])
-@pytest.mark.parametrize("T", [9, 2500])
 def test_rows_that_are_not_finite(bn, T, K, weighted, fused):
-    if T * K > 10 ** 7:
-        pytest.skip("the number of rows changes the threads per row only")
+    """Every width of the register form, and many rows, which take fewer threads each."""
     _not_finite(bn, T, K, weighted, False, fused)
